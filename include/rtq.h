@@ -284,6 +284,92 @@ rtq_status rtq_block_workspace_bytes(const rtq_block* blocks, int32_t n_blocks, 
 rtq_status rtq_block_project_ws(const rtq_block* blocks, int32_t n_blocks, int64_t M, int32_t math, void* workspace,
                                 int64_t workspace_bytes, void* stream);
 
+/* ---- 8-bit activations ----
+ *
+ * Rows of activations in 8 bits with one fp32 scale per row, and their product
+ * with the int8 and FP8 weights above on the 8-bit matrix cores. Element types
+ * of activations and outputs: RTQ_F32, RTQ_F16, RTQ_BF16. `fmt` of the codes:
+ * RTQ_FMT_Q8 (int8, largest code R = 127) or RTQ_FMT_F8 (E4M3, R = 448); the
+ * codes are one byte each, [M][K] contiguous.
+ *
+ * Codes and scales. A row of values r * p_k gets
+ *   code_k = the code nearest to R * p_k / P (ties to even), P = max_k |p_k|,
+ *   scale  = fp32(r * P / R),
+ * evaluated as in fp64 (the codes are those of the fp64 quotient, as the
+ * weight quantizers' are). A row of zeros gets scale 0 and codes 0. A row that
+ * holds an infinity or a NaN, or whose scale exceeds fp32, gets scale NaN and
+ * codes 0, so every product from it is NaN.
+ *
+ * Row strides (ldx, ...) count elements, are at least K, and let a row lie in a
+ * wider buffer; rows need no alignment beyond the element's. Outputs other
+ * than `sum` and y are contiguous. Memory ranges are taken as one interval
+ * from the first row to the last: two halves of one buffer may both be inputs,
+ * but no output may lie between an input's rows. K below 2^30.
+ *
+ * All of these allocate nothing, use no workspace and keep no state, so calls
+ * on different streams do not disturb each other and every call may be
+ * captured in a HIP graph. Results do not depend on the launch: the same
+ * inputs give the same bits. */
+enum { RTQ_F32 = 0, RTQ_F16 = 1, RTQ_BF16 = 2 };
+
+/* Quantizes rows: p = x, r = 1. */
+rtq_status rtq_quantize_rows(const void* x, int64_t ldx, int32_t dtype, int32_t fmt, void* codes, float* scale,
+                             int64_t M, int64_t K, void* stream);
+
+/* Root-mean-square norm. h = x + residual, added in fp32 and rounded once to
+ * the rows' type, is stored in `sum` and normalised; without a residual (NULL,
+ * and sum NULL) h = x. Then
+ *   y = h * weight / sqrt(mean(h^2) + eps),   the mean over the K of a row, in fp64.
+ * fmt RTQ_FMT_Q8 / RTQ_FMT_F8 writes codes [M][K] to `out` and scales (p = h *
+ * weight, r the row's factor); fmt RTQ_FMT_NONE writes y [M][K] to `out` in
+ * out_dtype (the rows' dtype or RTQ_F32; out_dtype is ignored otherwise) and
+ * takes scale NULL. weight is fp32 [K]; eps finite and positive. `sum` may be
+ * the residual or x itself (the same pointer and stride); it overlaps no
+ * input otherwise. */
+rtq_status rtq_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, void* sum, int64_t lds,
+                        const float* weight, float eps, int32_t dtype, int32_t fmt, int32_t out_dtype, void* out,
+                        float* scale, int64_t M, int64_t K, void* stream);
+
+/* Gated product: y = a / (1 + exp(-a)) * b, to codes and scales or dense, as
+ * rtq_rms_norm. Dense outputs are evaluated in fp32 and rounded once. */
+rtq_status rtq_silu_mul(const void* a, int64_t lda, const void* b, int64_t ldb, int32_t dtype, int32_t fmt,
+                        int32_t out_dtype, void* out, float* scale, int64_t M, int64_t K, void* stream);
+
+/* One projection of 8-bit rows: y[m][n] = x_scale[m] * scale[n] * sum_k
+ * x[m][k] * payload[n][k] (+ bias[n]), y in y_dtype with row stride ldy >= N.
+ * fmt RTQ_FMT_Q8: int8 rows and an int8 weight with its scales; the sum is
+ * exact in int32. RTQ_FMT_F8: E4M3 rows and weight, scale ignored (may be
+ * NULL); with y_dtype RTQ_F32 the sum is one of exact products in fp32, with a
+ * 16-bit y it runs on the FP8 matrix instructions at twice the rate, whose
+ * sums are within 2^-10 of sum|x w| (1e-5 of the result's norm on normal
+ * data). Scales, bias and one rounding to
+ * y_dtype are applied in fp32. K is at most RTQ_A8_MAX_K. x and payload need
+ * no alignment; the fast route takes K a multiple of 16 with both 16-byte
+ * aligned, other shapes are correct and slower. x_scale, scale and bias are
+ * 4-byte aligned, y as its type. int4 weights are not taken (RTQ_ERR_FORMAT). */
+#define RTQ_A8_MAX_K 131071
+typedef struct rtq_proj_a8 {
+    int32_t fmt;
+    int32_t N;
+    int32_t K;
+    int32_t y_dtype;
+    const void* x;
+    const float* x_scale;
+    const void* payload;
+    const float* scale;
+    void* y;
+    int64_t ldy;
+    const float* bias;
+} rtq_proj_a8;
+
+/* rtq_project_a8: n (1..RTQ_MAX_BLOCKS * 8) projections of M rows each in as
+ * few launches as the argument limit allows, on one stream. `projs` is a HOST
+ * array, free as soon as the call returns. Projections may share x and
+ * weights; no y may overlap another's y or any input (several y may be columns
+ * of one buffer, with the same ldy). rtq_gemm_a8: one of them. */
+rtq_status rtq_project_a8(const rtq_proj_a8* projs, int32_t n, int64_t M, void* stream);
+rtq_status rtq_gemm_a8(const rtq_proj_a8* proj, int64_t M, void* stream);
+
 /* Kernel timing (profiling aid). While enabled, every main GEMM kernel launch
  * of the entry points above is bracketed by a pair of HIP events recorded on
  * its stream (events are created on first use and kept for reuse). Enabling

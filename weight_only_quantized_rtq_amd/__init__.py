@@ -10,6 +10,7 @@ model card, section "FP8 Format"):
   Q4Weight(payload uint8 [N, K/2], pairs float16 [N, K/32, 2])   (scale, min)
   Q8Weight(payload int8 [N, K],    scale float32 [N])
   F8Weight(payload uint8 [N, K])   E4M3 ("float8_e4m3fn") codes, no scale
+8-bit activations (module a8): A8Rows(codes [M, K], scale float32 [M]).
 """
 from __future__ import annotations
 
@@ -43,7 +44,8 @@ EXPORTS = ("rtq_gemm_q4", "rtq_gemm_q8", "rtq_gemm_f8", "rtq_block_project", "rt
            "rtq_dequant_q8", "rtq_dequant_f8", "rtq_quantize_q4", "rtq_quantize_q8", "rtq_quantize_f8",
            "rtq_quantize_q4_host", "rtq_quantize_q8_host", "rtq_quantize_f8_host", "rtq_gemm_ex",
            "rtq_block_project_ex", "rtq_block_project_noalloc", "rtq_block_workspace_bytes",
-           "rtq_block_project_ws", "rtq_diag_stream_read", "rtq_diag_mfma_loop", "rtq_timing_enable",
+           "rtq_block_project_ws", "rtq_quantize_rows", "rtq_rms_norm", "rtq_silu_mul", "rtq_project_a8",
+           "rtq_gemm_a8", "rtq_diag_stream_read", "rtq_diag_mfma_loop", "rtq_timing_enable",
            "rtq_timing_read", "rtq_status_string", "rtq_last_error", "rtq_version")
 
 # Arithmetic of a GEMM call (the `math` argument; None runs the library's
@@ -112,6 +114,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.rtq_block_workspace_bytes.restype = ctypes.c_int
     lib.rtq_block_project_ws.argtypes = [ctypes.POINTER(_Block), i32, i64, i32, vp, i64, vp]
     lib.rtq_block_project_ws.restype = ctypes.c_int
+    lib.rtq_quantize_rows.argtypes = [vp, i64, i32, i32, vp, vp, i64, i64, vp]
+    lib.rtq_quantize_rows.restype = ctypes.c_int
+    lib.rtq_rms_norm.argtypes = [vp, i64, vp, i64, vp, i64, vp, ctypes.c_float, i32, i32, i32, vp, vp, i64, i64, vp]
+    lib.rtq_rms_norm.restype = ctypes.c_int
+    lib.rtq_silu_mul.argtypes = [vp, i64, vp, i64, i32, i32, i32, vp, vp, i64, i64, vp]
+    lib.rtq_silu_mul.restype = ctypes.c_int
+    lib.rtq_project_a8.argtypes = [vp, i32, i64, vp]
+    lib.rtq_project_a8.restype = ctypes.c_int
+    lib.rtq_gemm_a8.argtypes = [vp, i64, vp]
+    lib.rtq_gemm_a8.restype = ctypes.c_int
     lib.rtq_diag_stream_read.argtypes = [vp, i64, i32, i32, vp, vp]
     lib.rtq_diag_stream_read.restype = ctypes.c_int
     lib.rtq_diag_mfma_loop.argtypes = [i32, i64, i32, vp, ctypes.POINTER(ctypes.c_double), vp]
@@ -428,8 +440,8 @@ def quantize(W: torch.Tensor, fmt: str, stream=None):
 class Projection:
     """One projection of a block: its weight, the input it reads and the output it writes."""
     weight: object               # Q4Weight | Q8Weight | F8Weight
-    x: torch.Tensor              # float32 [M, K]
-    y: torch.Tensor              # float32 [M, N]
+    x: torch.Tensor              # float32 [M, K] (project_a8: A8Rows)
+    y: torch.Tensor              # float32 [M, N] (project_a8: also float16, bfloat16)
     bias: torch.Tensor | None = None   # float32 [N], added to every row of y
 
 
@@ -496,3 +508,7 @@ def block_project(blocks: list[dict[str, Projection]], M: int, stream=None, pack
         _check(lib.rtq_block_project(arr, len(arr), M, _stream(stream)))
     else:
         _check(lib.rtq_block_project_ex(arr, len(arr), M, int(math), _stream(stream)))
+
+
+from .a8 import (A8Rows, ffn_a8, gemm_a8, project_a8, quantize_rows,  # noqa: E402
+                 rms_norm, silu_mul)

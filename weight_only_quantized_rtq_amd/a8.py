@@ -1,0 +1,274 @@
+"""8-bit activations: row operators that write codes with a scale per row, and
+the product of such rows with the int8 and FP8 weights.
+
+    rows, h = rms_norm(x, weight, residual=res, fmt="q8")   # A8Rows, x + res
+    y = gemm_a8(rows, w)                                    # w: Q8Weight (or F8Weight with fmt="f8")
+
+Argument marshalling only, as the rest of the binding. Activations are
+float32, float16 or bfloat16 [M, K] tensors whose rows may lie in a wider
+buffer (stride(1) == 1). Where `out`, `sum_out` or `y` is not given it is
+allocated on the call's stream. `stream` runs the call on another stream than
+the current one; ordering the inputs before it, and what uses the outputs
+after it, is the caller's part, as everywhere in torch. Nothing here records
+gradients.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from dataclasses import dataclass
+
+import torch
+
+from . import FMT_F8, FMT_NONE, FMT_Q8, MAX_BLOCKS, F8Weight, Projection, Q8Weight, _check, _need, _stream, load_library
+
+A8_MAX_K = 131071
+_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_FMTS = {None: FMT_NONE, "q8": FMT_Q8, "f8": FMT_F8}
+_CODES = {FMT_Q8: torch.int8, FMT_F8: torch.uint8}
+
+
+class _ProjA8(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("y_dtype", ctypes.c_int32),
+                ("x", ctypes.c_void_p), ("x_scale", ctypes.c_void_p), ("payload", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+                ("bias", ctypes.c_void_p)]
+
+
+@dataclass
+class A8Rows:
+    """Rows of activations in 8 bits: row m holds scale[m] * codes[m]."""
+    codes: torch.Tensor      # int8 [M, K], or uint8 [M, K]: E4M3 codes
+    scale: torch.Tensor      # float32 [M]
+
+    @property
+    def M(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def K(self) -> int:
+        return self.codes.shape[1]
+
+    @property
+    def fmt(self) -> int:
+        return FMT_Q8 if self.codes.dtype == torch.int8 else FMT_F8
+
+    def validate(self) -> None:
+        _need(self.codes, torch.int8 if self.codes.dtype == torch.int8 else torch.uint8, "codes")
+        _need(self.scale, torch.float32, "scale")
+        if self.codes.dim() != 2 or tuple(self.scale.shape) != (self.codes.shape[0],):
+            raise ValueError(f"8-bit row shapes disagree: codes {tuple(self.codes.shape)}, "
+                             f"scale {tuple(self.scale.shape)}")
+
+    def dequant(self) -> torch.Tensor:
+        """The float32 values [M, K] the rows stand for."""
+        codes = self.codes if self.codes.dtype == torch.int8 else self.codes.view(torch.float8_e4m3fn)
+        return codes.to(torch.float32) * self.scale[:, None]
+
+
+def _rows(t, name: str, shape=None, dtype=None) -> int:
+    """Checks a [M, K] tensor whose rows may be strided; returns the row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _DTYPES if dtype is None else t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype or 'float32, float16 or bfloat16'}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be {'[M, K]' if shape is None else list(shape)}, got {list(t.shape)}")
+    M, K = t.shape
+    ld, step = t.stride()
+    if step != 1 and K > 1:
+        raise ValueError(f"{name}: the elements of a row must be adjacent, stride {t.stride()}")
+    if M <= 1:
+        return K
+    if ld < K:
+        raise ValueError(f"{name}: rows overlap, stride {t.stride()}")
+    return ld
+
+
+def _on(stream):
+    """The context new outputs are allocated in: the stream the call runs on."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+
+
+def _fmt(fmt) -> int:
+    try:
+        return _FMTS[fmt]
+    except KeyError:
+        raise ValueError(f"unknown format {fmt!r}") from None
+
+
+def _row_out(out, M: int, K: int, x, fmt: int, out_dtype, stream):
+    """The output of a row operator, checked or new: (object to return, its
+    pointer, the scale's pointer, its dtype code)."""
+    if fmt == FMT_NONE:
+        if out is None:
+            out_dtype = x.dtype if out_dtype is None else out_dtype
+            if out_dtype not in (x.dtype, torch.float32):
+                raise TypeError(f"out_dtype must be {x.dtype} or float32, got {out_dtype}")
+            with _on(stream):
+                out = torch.empty((M, K), dtype=out_dtype, device=x.device)
+        else:
+            if not isinstance(out, torch.Tensor) or out.dtype not in (x.dtype, torch.float32) \
+                    or out_dtype not in (None, out.dtype):
+                raise TypeError(f"out must be a {x.dtype} or float32 tensor (of out_dtype, where that is given)")
+            _need(out, out.dtype, "out")
+            if out.shape != (M, K):
+                raise ValueError(f"out must be [{M}, {K}], got {list(out.shape)}")
+        return out, out.data_ptr(), None, _DTYPES[out.dtype]
+    if out_dtype is not None:
+        raise TypeError("out_dtype is for dense output (fmt None)")
+    if out is None:
+        with _on(stream):
+            out = A8Rows(torch.empty((M, K), dtype=_CODES[fmt], device=x.device),
+                         torch.empty((M,), dtype=torch.float32, device=x.device))
+    else:
+        if not isinstance(out, A8Rows):
+            raise TypeError("out must be an A8Rows")
+        _need(out.codes, _CODES[fmt], "out.codes")
+        _need(out.scale, torch.float32, "out.scale")
+        if out.codes.shape != (M, K) or out.scale.shape != (M,):
+            raise ValueError(f"out must hold [{M}, {K}] codes and [{M}] scales, got {list(out.codes.shape)} and "
+                             f"{list(out.scale.shape)}")
+    return out, out.codes.data_ptr(), out.scale.data_ptr(), 0
+
+
+def quantize_rows(x: torch.Tensor, fmt: str = "q8", out: A8Rows | None = None, stream=None) -> A8Rows:
+    """Rows of x in 8 bits (rtq_quantize_rows): "q8" int8, "f8" E4M3."""
+    lib = load_library()
+    code = _fmt(fmt)
+    if code == FMT_NONE:
+        raise ValueError('quantize_rows writes "q8" or "f8"')
+    ld = _rows(x, "x")
+    M, K = x.shape
+    out, p, s, _ = _row_out(out, M, K, x, code, None, stream)
+    _check(lib.rtq_quantize_rows(x.data_ptr(), ld, _DTYPES[x.dtype], code, p, s, M, K, _stream(stream)))
+    return out
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
+             fmt: str | None = None, out=None, sum_out: torch.Tensor | None = None, out_dtype=None, stream=None):
+    """Root-mean-square norm of x (or of h = x + residual) times the float32
+    weight [K] (rtq_rms_norm). fmt "q8" / "f8" returns A8Rows, None a dense
+    tensor of out_dtype (x's dtype, the default, or float32). With a residual
+    the result is (output, h); sum_out holds h and may be x or residual itself."""
+    lib = load_library()
+    code = _fmt(fmt)
+    ld = _rows(x, "x")
+    M, K = x.shape
+    _need(weight, torch.float32, "weight")
+    if weight.shape != (K,):
+        raise ValueError(f"weight must be [{K}], got {list(weight.shape)}")
+    ldr = lds = 0
+    if residual is not None:
+        ldr = _rows(residual, "residual", x.shape, x.dtype)
+        if sum_out is None:
+            with _on(stream):
+                sum_out = torch.empty((M, K), dtype=x.dtype, device=x.device)
+        lds = _rows(sum_out, "sum_out", x.shape, x.dtype)
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    out, p, s, out_code = _row_out(out, M, K, x, code, out_dtype, stream)
+    _check(lib.rtq_rms_norm(x.data_ptr(), ld, None if residual is None else residual.data_ptr(), ldr,
+                            None if residual is None else sum_out.data_ptr(), lds, weight.data_ptr(), eps,
+                            _DTYPES[x.dtype], code, out_code, p, s, M, K, _stream(stream)))
+    return out if residual is None else (out, sum_out)
+
+
+def silu_mul(a: torch.Tensor, b: torch.Tensor, fmt: str | None = None, out=None, out_dtype=None, stream=None):
+    """silu(a) * b (rtq_silu_mul): A8Rows for fmt "q8" / "f8", else dense."""
+    lib = load_library()
+    code = _fmt(fmt)
+    lda = _rows(a, "a")
+    ldb = _rows(b, "b", a.shape, a.dtype)
+    M, K = a.shape
+    out, p, s, out_code = _row_out(out, M, K, a, code, out_dtype, stream)
+    _check(lib.rtq_silu_mul(a.data_ptr(), lda, b.data_ptr(), ldb, _DTYPES[a.dtype], code, out_code, p, s, M, K,
+                            _stream(stream)))
+    return out
+
+
+def _pack(d: _ProjA8, x: A8Rows, w, y: torch.Tensor, bias) -> None:
+    if not isinstance(x, A8Rows):
+        raise TypeError("x must be an A8Rows (quantize_rows, rms_norm or silu_mul with a format)")
+    if not isinstance(w, (Q8Weight, F8Weight)):
+        raise TypeError(f"8-bit rows multiply a Q8Weight or an F8Weight, got {type(w).__name__}")
+    x.validate()
+    w.validate()
+    if x.fmt != w.fmt:
+        raise TypeError(f"{'int8' if x.fmt == FMT_Q8 else 'E4M3'} rows do not multiply a {type(w).__name__}")
+    if x.K != w.K:
+        raise ValueError(f"x must be [M, {w.K}], got {list(x.codes.shape)}")
+    d.fmt, d.N, d.K = w.fmt, w.N, w.K
+    d.ldy = _rows(y, "y", (x.M, w.N))
+    d.y_dtype = _DTYPES[y.dtype]
+    d.x, d.x_scale = x.codes.data_ptr(), x.scale.data_ptr()
+    d.payload = w.payload.data_ptr()
+    d.scale = w.scale.data_ptr() if w.fmt == FMT_Q8 else None
+    d.y = y.data_ptr()
+    if bias is not None:
+        _need(bias, torch.float32, "bias")
+        if bias.shape != (w.N,):
+            raise ValueError(f"bias {list(bias.shape)} does not match N={w.N}")
+        d.bias = bias.data_ptr()
+
+
+def gemm_a8(x: A8Rows, w, y: torch.Tensor | None = None, bias: torch.Tensor | None = None, out_dtype=None,
+            stream=None) -> torch.Tensor:
+    """y = x . W^T (+ bias) for 8-bit rows and a Q8Weight or F8Weight of the same
+    format (rtq_gemm_a8). y is float32 unless out_dtype (or y itself) says otherwise."""
+    lib = load_library()
+    if y is None:
+        if not isinstance(x, A8Rows):
+            raise TypeError("x must be an A8Rows (quantize_rows, rms_norm or silu_mul with a format)")
+        out_dtype = torch.float32 if out_dtype is None else out_dtype
+        if out_dtype not in _DTYPES:
+            raise TypeError(f"out_dtype must be float32, float16 or bfloat16, got {out_dtype}")
+        with _on(stream):
+            y = torch.empty((x.M, w.N), dtype=out_dtype, device=x.codes.device)
+    elif out_dtype not in (None, y.dtype):
+        raise TypeError(f"y is {y.dtype}, out_dtype {out_dtype}")
+    d = _ProjA8()
+    _pack(d, x, w, y, bias)
+    _check(lib.rtq_gemm_a8(ctypes.byref(d), x.M, _stream(stream)))
+    return y
+
+
+def project_a8(projections: list[Projection], stream=None) -> None:
+    """Several projections of 8-bit rows in one call (rtq_project_a8): each
+    Projection's x is an A8Rows, all of them with the same number of rows, and
+    its y a float32, float16 or bfloat16 tensor that may be columns of a wider one."""
+    lib = load_library()
+    if not 1 <= len(projections) <= MAX_BLOCKS * 8:
+        raise ValueError(f"1..{MAX_BLOCKS * 8} projections per call, got {len(projections)}")
+    arr = (_ProjA8 * len(projections))()
+    for d, p in zip(arr, projections):
+        _pack(d, p.x, p.weight, p.y, p.bias)
+        if p.x.M != projections[0].x.M:
+            raise ValueError(f"the projections of one call share M: {p.x.M} and {projections[0].x.M}")
+    _check(lib.rtq_project_a8(arr, len(arr), projections[0].x.M, _stream(stream)))
+
+
+def ffn_a8(x: torch.Tensor, weight: torch.Tensor, w1, w3, w2, eps: float = 1e-6,
+           residual: torch.Tensor | None = None, stream=None):
+    """A gated FFN on 8-bit rows: with n = rms_norm(x (+ residual), weight),
+    (silu(n . W1^T) * (n . W3^T)) . W2^T, every product on 8-bit rows of the
+    weights' format. Returns y [M, w2.N] in x's dtype, or (y, x + residual)."""
+    if not isinstance(w1, (Q8Weight, F8Weight)):
+        raise TypeError(f"8-bit rows multiply a Q8Weight or an F8Weight, got {type(w1).__name__}")
+    fmt = "q8" if w1.fmt == FMT_Q8 else "f8"
+    rows = rms_norm(x, weight, eps, residual=residual, fmt=fmt, stream=stream)
+    h = None
+    if residual is not None:
+        rows, h = rows
+    with _on(stream):
+        ab = torch.empty((x.shape[0], w1.N + w3.N), dtype=x.dtype, device=x.device)
+    a, b = ab[:, :w1.N], ab[:, w1.N:]
+    project_a8([Projection(w1, rows, a), Projection(w3, rows, b)], stream)
+    y = gemm_a8(silu_mul(a, b, fmt=fmt, stream=stream), w2, out_dtype=x.dtype, stream=stream)
+    return y if h is None else (y, h)

@@ -430,6 +430,205 @@ rtq_status rtq_quantize_f8(const float* w, uint8_t* codes, int64_t N, int64_t K,
                       "rtq_quantize_f8 launch");
 }
 
+// ---- 8-bit activations ----
+namespace {
+
+// Bytes of an element of an activation type; 0 for an unknown one.
+int dtype_bytes(int32_t dtype) { return dtype == RTQ_F32 ? 4 : dtype == RTQ_F16 || dtype == RTQ_BF16 ? 2 : 0; }
+
+bool a8_fmt(int32_t fmt) { return fmt == RTQ_FMT_Q8 || fmt == RTQ_FMT_F8; }
+
+rtq_status check_mk(const char* name, int64_t M, int64_t K) {
+    if (M < 0 || M > kMaxDim) return fail(RTQ_ERR_SHAPE, "%s: M=%lld out of range [0, 2^30)", name, (long long)M);
+    if (K < 1 || K > kMaxDim) return fail(RTQ_ERR_SHAPE, "%s: K=%lld out of range [1, 2^30)", name, (long long)K);
+    if (M * K > kMaxElems)
+        return fail(RTQ_ERR_SHAPE, "%s: M=%lld K=%lld exceed 2^38 elements", name, (long long)M, (long long)K);
+    return RTQ_OK;
+}
+
+// M rows of K elements of `size` bytes at stride ld: checks, and the interval
+// of memory that they lie in.
+rtq_status check_rows(const char* name, const char* arg, const void* p, int64_t ld, int size, int64_t M, int64_t K,
+                      Range* r) {
+    if (!p) return fail(RTQ_ERR_NULL, "%s: %s is NULL", name, arg);
+    if (!aligned(p, size)) return fail(RTQ_ERR_ALIGN, "%s: %s is not %d-byte aligned", name, arg, size);
+    if (ld < K) return fail(RTQ_ERR_SHAPE, "%s: the row stride %lld of %s is below %lld", name, (long long)ld, arg, (long long)K);
+    // M and ld are below 2^31 wherever the product is formed
+    if (ld > kMaxElems || (M > 1 && ld > kMaxElems / M))
+        return fail(RTQ_ERR_SHAPE, "%s: the row stride %lld of %s exceeds 2^38 elements", name, (long long)ld, arg);
+    *r = range_of(p, ((M - 1) * ld + K) * size);
+    return RTQ_OK;
+}
+
+// The output of a row operator: codes and scales, or dense rows.
+rtq_status check_row_out(const char* name, int32_t dtype, int32_t fmt, int32_t out_dtype, const void* out,
+                         const float* scale, int64_t M, int64_t K, Range* o, Range* s) {
+    *s = Range{0, 0};
+    if (fmt == RTQ_FMT_NONE) {
+        if (out_dtype != RTQ_F32 && out_dtype != dtype)
+            return fail(RTQ_ERR_FORMAT, "%s: out_dtype %d is neither fp32 nor the rows' type", name, out_dtype);
+        if (scale) return fail(RTQ_ERR_FORMAT, "%s: dense output takes no scale", name);
+        return check_rows(name, "out", out, K, dtype_bytes(out_dtype), M, K, o);
+    }
+    if (!a8_fmt(fmt)) return fail(RTQ_ERR_FORMAT, "%s: unknown fmt %d", name, fmt);
+    Range t;
+    rtq_status st = check_rows(name, "out", out, K, 1, M, K, o);
+    if (st != RTQ_OK) return st;
+    st = check_rows(name, "scale", scale, 1, 4, M, 1, &t);
+    if (st != RTQ_OK) return st;
+    *s = t;
+    if (overlaps(*o, *s)) return fail(RTQ_ERR_OVERLAP, "%s: out and scale overlap", name);
+    return RTQ_OK;
+}
+
+// Rows of one output of rtq_project_a8, in bytes.
+struct OutRows {
+    Range r;
+    uintptr_t stride, width, top;
+};
+
+// Whether two outputs with a.r.lo <= b.r.lo are columns of one wider buffer:
+// the same stride, and b's columns in the gap between a's rows.
+bool side_by_side(const OutRows& a, const OutRows& b) {
+    if (a.stride != b.stride) return false;
+    const uintptr_t at = (b.r.lo - a.r.lo) % a.stride;
+    return at >= a.width && at + b.width <= a.stride;
+}
+
+rtq_status check_no_overlap(const char* name, Range o, Range s, const Range* ins, int n) {
+    for (int i = 0; i < n; ++i)
+        if (overlaps(o, ins[i]) || overlaps(s, ins[i]))
+            return fail(RTQ_ERR_OVERLAP, "%s: an output overlaps an input or the sum", name);
+    return RTQ_OK;
+}
+
+}  // namespace
+
+rtq_status rtq_quantize_rows(const void* x, int64_t ldx, int32_t dtype, int32_t fmt, void* codes, float* scale,
+                             int64_t M, int64_t K, void* stream) {
+    static const char* name = "rtq_quantize_rows";
+    clear_error();
+    if (!dtype_bytes(dtype)) return fail(RTQ_ERR_FORMAT, "%s: unknown dtype %d", name, dtype);
+    if (!a8_fmt(fmt)) return fail(RTQ_ERR_FORMAT, "%s: unknown fmt %d", name, fmt);
+    rtq_status st = check_mk(name, M, K);
+    if (st != RTQ_OK || M == 0) return st;
+    Range in, o, s;
+    if ((st = check_rows(name, "x", x, ldx, dtype_bytes(dtype), M, K, &in)) != RTQ_OK) return st;
+    if ((st = check_row_out(name, dtype, fmt, 0, codes, scale, M, K, &o, &s)) != RTQ_OK) return st;
+    if ((st = check_no_overlap(name, o, s, &in, 1)) != RTQ_OK) return st;
+    return hip_status(rtq::launch_quantize_rows(x, ldx, dtype, fmt, codes, scale, M, K, static_cast<hipStream_t>(stream)),
+                      "rtq_quantize_rows launch");
+}
+
+rtq_status rtq_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, void* sum, int64_t lds,
+                        const float* weight, float eps, int32_t dtype, int32_t fmt, int32_t out_dtype, void* out,
+                        float* scale, int64_t M, int64_t K, void* stream) {
+    static const char* name = "rtq_rms_norm";
+    clear_error();
+    const int size = dtype_bytes(dtype);
+    if (!size) return fail(RTQ_ERR_FORMAT, "%s: unknown dtype %d", name, dtype);
+    rtq_status st = check_mk(name, M, K);
+    if (st != RTQ_OK) return st;
+    if (!(eps > 0.0f) || eps > 3.402823466e38f) return fail(RTQ_ERR_SHAPE, "%s: eps must be finite and positive", name);
+    if (!residual != !sum) return fail(RTQ_ERR_NULL, "%s: residual and sum come together", name);
+    if (M == 0) return RTQ_OK;
+    Range ins[4], o, s;
+    int n = 0;
+    if ((st = check_rows(name, "x", x, ldx, size, M, K, &ins[n++])) != RTQ_OK) return st;
+    if ((st = check_rows(name, "weight", weight, K, 4, 1, K, &ins[n++])) != RTQ_OK) return st;
+    if (residual) {
+        if ((st = check_rows(name, "residual", residual, ldr, size, M, K, &ins[n++])) != RTQ_OK) return st;
+        if ((st = check_rows(name, "sum", sum, lds, size, M, K, &ins[n++])) != RTQ_OK) return st;
+        const bool is_x = sum == x && lds == ldx, is_r = sum == residual && lds == ldr;
+        if ((!is_x && overlaps(ins[3], ins[0])) || (!is_r && overlaps(ins[3], ins[2])) || overlaps(ins[3], ins[1]))
+            return fail(RTQ_ERR_OVERLAP, "%s: sum overlaps an input it is not equal to", name);
+        if (M > 1 && lds < K) return fail(RTQ_ERR_SHAPE, "%s: rows of sum overlap", name);
+    }
+    if ((st = check_row_out(name, dtype, fmt, out_dtype, out, scale, M, K, &o, &s)) != RTQ_OK) return st;
+    if ((st = check_no_overlap(name, o, s, ins, n)) != RTQ_OK) return st;
+    return hip_status(rtq::launch_rms_norm(x, ldx, residual, ldr, sum, lds, weight, eps, dtype, fmt, out_dtype, out,
+                                           scale, M, K, static_cast<hipStream_t>(stream)),
+                      "rtq_rms_norm launch");
+}
+
+rtq_status rtq_silu_mul(const void* a, int64_t lda, const void* b, int64_t ldb, int32_t dtype, int32_t fmt,
+                        int32_t out_dtype, void* out, float* scale, int64_t M, int64_t K, void* stream) {
+    static const char* name = "rtq_silu_mul";
+    clear_error();
+    const int size = dtype_bytes(dtype);
+    if (!size) return fail(RTQ_ERR_FORMAT, "%s: unknown dtype %d", name, dtype);
+    rtq_status st = check_mk(name, M, K);
+    if (st != RTQ_OK || M == 0) return st;
+    Range ins[2], o, s;
+    if ((st = check_rows(name, "a", a, lda, size, M, K, &ins[0])) != RTQ_OK) return st;
+    if ((st = check_rows(name, "b", b, ldb, size, M, K, &ins[1])) != RTQ_OK) return st;
+    if ((st = check_row_out(name, dtype, fmt, out_dtype, out, scale, M, K, &o, &s)) != RTQ_OK) return st;
+    if ((st = check_no_overlap(name, o, s, ins, 2)) != RTQ_OK) return st;
+    return hip_status(rtq::launch_silu_mul(a, lda, b, ldb, dtype, fmt, out_dtype, out, scale, M, K,
+                                           static_cast<hipStream_t>(stream)),
+                      "rtq_silu_mul launch");
+}
+
+rtq_status rtq_project_a8(const rtq_proj_a8* projs, int32_t n, int64_t M, void* stream) {
+    clear_error();
+    static const char* what = "rtq_project_a8";
+    constexpr int kMost = RTQ_MAX_BLOCKS * 8;
+    if (!projs) return fail(RTQ_ERR_NULL, "%s: projs is NULL", what);
+    if (n < 1 || n > kMost) return fail(RTQ_ERR_SHAPE, "%s: n=%d out of range [1, %d]", what, n, kMost);
+    if (M < 0 || M > kMaxDim) return fail(RTQ_ERR_SHAPE, "%s: M=%lld out of range [0, 2^30)", what, (long long)M);
+    // Per-thread arrays of the largest call.
+    thread_local rtq::A8Task tasks[kMost];
+    thread_local OutRows outs[kMost];
+    thread_local Range ins[kMost * 5];
+    int n_ins = 0;
+    for (int i = 0; i < n; ++i) {
+        const rtq_proj_a8& d = projs[i];
+        char name[48];
+        std::snprintf(name, sizeof(name), "%s: projection %d", what, i);
+        if (!a8_fmt(d.fmt)) return fail(RTQ_ERR_FORMAT, "%s: fmt %d is not int8 or FP8", name, d.fmt);
+        const int size = dtype_bytes(d.y_dtype);
+        if (!size) return fail(RTQ_ERR_FORMAT, "%s: unknown y_dtype %d", name, d.y_dtype);
+        if (d.N < 1 || d.N > kMaxDim) return fail(RTQ_ERR_SHAPE, "%s: N=%d out of range [1, 2^30)", name, d.N);
+        if (d.K < 1 || d.K > RTQ_A8_MAX_K)
+            return fail(RTQ_ERR_SHAPE, "%s: K=%d out of range [1, %d]", name, d.K, RTQ_A8_MAX_K);
+        if (M * d.N > kMaxElems || M * d.K > kMaxElems || int64_t(d.N) * d.K > kMaxElems)
+            return fail(RTQ_ERR_SHAPE, "%s: M=%lld N=%d K=%d exceed 2^38 elements in one tensor", name, (long long)M,
+                        d.N, d.K);
+        if (M == 0) continue;
+        rtq_status st;
+        if ((st = check_rows(name, "x", d.x, d.K, 1, M, d.K, &ins[n_ins++])) != RTQ_OK) return st;
+        if ((st = check_rows(name, "x_scale", d.x_scale, 1, 4, M, 1, &ins[n_ins++])) != RTQ_OK) return st;
+        if ((st = check_rows(name, "payload", d.payload, d.K, 1, d.N, d.K, &ins[n_ins++])) != RTQ_OK) return st;
+        if (d.fmt == RTQ_FMT_Q8 && (st = check_rows(name, "scale", d.scale, d.N, 4, 1, d.N, &ins[n_ins++])) != RTQ_OK) return st;
+        if (d.bias && (st = check_rows(name, "bias", d.bias, d.N, 4, 1, d.N, &ins[n_ins++])) != RTQ_OK) return st;
+        if ((st = check_rows(name, "y", d.y, d.ldy, size, M, d.N, &outs[i].r)) != RTQ_OK) return st;
+        outs[i].stride = static_cast<uintptr_t>(d.ldy) * size;
+        outs[i].width = static_cast<uintptr_t>(d.N) * size;
+        tasks[i] = rtq::A8Task{static_cast<const uint8_t*>(d.x), d.x_scale, static_cast<const uint8_t*>(d.payload),
+                               d.fmt == RTQ_FMT_Q8 ? d.scale : nullptr, d.bias, d.y, d.ldy, d.N, d.K, d.y_dtype,
+                               d.fmt == RTQ_FMT_Q8 ? rtq::kA8Int : d.y_dtype == RTQ_F32 ? rtq::kA8F8Wide : rtq::kA8F8};
+    }
+    if (M == 0) return RTQ_OK;
+    // Outputs sorted by their first byte; top = the furthest end so far, so an
+    // input meets some output's interval iff one that begins before the
+    // input's end reaches past its start.
+    std::sort(outs, outs + n, [](const OutRows& a, const OutRows& b) { return a.r.lo < b.r.lo; });
+    for (int i = 0; i < n; ++i) {
+        outs[i].top = i && outs[i - 1].top > outs[i].r.hi ? outs[i - 1].top : outs[i].r.hi;
+        for (int j = i + 1; j < n && outs[j].r.lo < outs[i].r.hi; ++j)
+            if (!side_by_side(outs[i], outs[j]))
+                return fail(RTQ_ERR_OVERLAP, "%s: two projections write overlapping outputs", what);
+    }
+    for (int i = 0; i < n_ins; ++i) {
+        const OutRows* it = std::lower_bound(outs, outs + n, ins[i].hi,
+                                             [](const OutRows& o, uintptr_t v) { return o.r.lo < v; });
+        if (it != outs && it[-1].top > ins[i].lo) return fail(RTQ_ERR_OVERLAP, "%s: an output overlaps an input", what);
+    }
+    return hip_status(rtq::launch_a8(tasks, n, M, static_cast<hipStream_t>(stream)), "rtq_project_a8 launch");
+}
+
+rtq_status rtq_gemm_a8(const rtq_proj_a8* proj, int64_t M, void* stream) { return rtq_project_a8(proj, 1, M, stream); }
+
 // ---- diagnostics: measured ceilings ----
 rtq_status rtq_diag_stream_read(const void* buf, int64_t bytes, int32_t unroll, int32_t blocks, uint32_t* sink,
                                 void* stream) {

@@ -98,6 +98,42 @@ void quantize_f8_host(const float* w, uint8_t* codes, int64_t N, int64_t K, int 
 // place, after the GEMM kernels that wrote y (same stream).
 hipError_t launch_bias_add(const ProjTask* tasks, int count, int64_t M, hipStream_t stream);
 
+// Row operators (rows.hip): fmt kFmtQ8 / kFmtF8 writes codes and scale, fmt 0
+// dense rows of out_dtype (the input's dtype or RTQ_F32). Strides in elements.
+hipError_t launch_quantize_rows(const void* x, int64_t ldx, int dtype, int fmt, void* codes, float* scale, int64_t M,
+                                int64_t K, hipStream_t stream);
+hipError_t launch_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, void* sum, int64_t lds,
+                           const float* weight, float eps, int dtype, int fmt, int out_dtype, void* out, float* scale,
+                           int64_t M, int64_t K, hipStream_t stream);
+hipError_t launch_silu_mul(const void* x, int64_t lda, const void* b, int64_t ldb, int dtype, int fmt, int out_dtype,
+                           void* out, float* scale, int64_t M, int64_t K, hipStream_t stream);
+
+// 8-bit activations times 8-bit weights (gemm_a8.hip). Kinds of sums: int8;
+// E4M3 for 16-bit outputs; E4M3 in bf16 operands, for fp32 outputs.
+enum A8Kind : int { kA8Int = 0, kA8F8 = 1, kA8F8Wide = 2, kA8Kinds = 3 };
+struct A8Task {
+    const uint8_t* x;        // [M][K] codes
+    const float* x_scale;    // [M]
+    const uint8_t* w;        // [N][K] codes
+    const float* w_scale;    // [N], nullptr for FP8
+    const float* bias;       // [N] or nullptr
+    void* y;
+    int64_t ldy;             // elements
+    int32_t N;
+    int32_t K;
+    int32_t y_dtype;
+    int32_t kind;
+};
+constexpr int kA8Slots = 8;  // tasks of one launch
+struct A8Args {
+    A8Task task[kA8Slots];
+    int64_t M;
+    uint32_t begin[kA8Slots];    // first workgroup of each task
+    int32_t count;
+};
+// Tasks of any kinds, all sharing M.
+hipError_t launch_a8(const A8Task* tasks, int count, int64_t M, hipStream_t stream);
+
 // Diagnostics (diag.hip): measured ceilings.
 hipError_t launch_stream_read(const void* buf, int64_t bytes, int unroll, int blocks, uint32_t* sink,
                               hipStream_t stream);
