@@ -15,6 +15,8 @@
 //    v_mfma_f32_16x16x32_bf16, whose sums are fp32, at half the rate.
 #include <rtq.h>
 
+#include <type_traits>
+
 #include "rtq_internal.h"
 #include "split_device.h"
 
@@ -67,34 +69,13 @@ __device__ __forceinline__ typename Acc<KIND>::T mma(i32x4 a0, i32x4 a1, i32x4 b
     }
 }
 
-// Four outputs y[m][n .. n+3].
-__device__ __forceinline__ void store4(const A8Task& t, int64_t m, int64_t n, const float (&v)[4]) {
-    const int64_t at = m * t.ldy + n;
-    const int left = static_cast<int>(t.N - n < 4 ? t.N - n : 4);
-    auto put = [&](auto* y) {
-        typedef __remove_reference_t(decltype(*y)) T;
-        T w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = static_cast<T>(v[j]);
-        if (left == 4) {
-            __builtin_memcpy(y + at, w, sizeof(w));
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (j < left) y[at + j] = w[j];
-        }
-    };
-    if (t.y_dtype == RTQ_F32) put(static_cast<float*>(t.y));
-    else if (t.y_dtype == RTQ_F16) put(static_cast<_Float16*>(t.y));
-    else put(static_cast<__bf16*>(t.y));
-}
-
-// 16 bytes of a row at k (any alignment), zeros past K.
+// 16 bytes of a row at k, zeros past K. ALIGNED: K a multiple of 16.
+template <bool ALIGNED>
 __device__ __forceinline__ i32x4 load16(const uint8_t* row, int k, int K) {
     i32x4 v = {0, 0, 0, 0};
     if (k + 16 <= K) {
         __builtin_memcpy(&v, row + k, 16);
-    } else if (k < K) {
+    } else if (!ALIGNED && k < K) {
 #pragma unroll
         for (int j = 0; j < 15; ++j)
             if (k + j < K) v[j / 4] |= static_cast<int>(row[k + j]) << (8 * (j % 4));
@@ -102,90 +83,292 @@ __device__ __forceinline__ i32x4 load16(const uint8_t* row, int k, int K) {
     return v;
 }
 
-// LDS: rows of 128 bytes, the 16-byte chunk c of row r at slot c ^ (r & 7).
-__device__ __forceinline__ int lds_at(int r, int c) { return r * kBK + ((c ^ (r & 7)) << 4); }
-
-template <int KIND, int BM, int BN>
-__global__ __launch_bounds__(256) void tile_kernel(const A8Args args) {
-    constexpr int WM = BM / 2, WN = BN / 2;                    // four waves, 2 x 2
-    __shared__ __align__(16) uint8_t sx[BM * kBK];
-    __shared__ __align__(16) uint8_t sw[BN * kBK];
+// The workgroup's task and its number among the task's workgroups.
+__device__ __forceinline__ const A8Task& task_of(const A8Args& args, uint32_t w, int& at) {
     int j = 0;
-    while (j + 1 < args.count && static_cast<uint32_t>(args.begin[j + 1]) <= blockIdx.x) ++j;
-    const A8Task& t = args.task[j];
-    const int tile = blockIdx.x - args.begin[j];
-    const int tiles_n = (t.N + BN - 1) / BN;
-    const int64_t m0 = static_cast<int64_t>(tile / tiles_n) * BM;
-    const int64_t n0 = static_cast<int64_t>(tile % tiles_n) * BN;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = (wave & 1) * WM, wn = (wave >> 1) * WN;
-    const int r16 = lane & 15, g = lane >> 4;
-    typename Acc<KIND>::T acc[WN / 16][WM / 16] = {};
+#pragma unroll
+    for (int i = 1; i < kA8Slots; ++i) j += i < args.count && args.begin[i] <= w;
+    j = __builtin_amdgcn_readfirstlane(j);
+    at = static_cast<int>(w - args.begin[j]);
+    return args.task[j];
+}
 
-    for (int k0 = 0; k0 < t.K; k0 += kBK) {
-        __syncthreads();
+// Four fp32 values of a vector at n, those past N from its last element; `none` without a vector.
+__device__ __forceinline__ floatx4 channels(const float* p, int n, int N, float none) {
+    floatx4 v = {none, none, none, none};
+    if (!p) return v;
+    if (n + 4 <= N) {
+        __builtin_memcpy(&v, p + n, 16);
+    } else {
 #pragma unroll
-        for (int i = 0; i < BM * 8 / 256; ++i) {
-            const int at = i * 256 + threadIdx.x, r = at >> 3, c = at & 7;
-            const int64_t m = m0 + r < args.M ? m0 + r : args.M - 1;       // rows past the end: not stored
-            *reinterpret_cast<i32x4*>(sx + lds_at(r, c)) = load16(t.x + m * t.K, k0 + c * 16, t.K);
-        }
+        for (int e = 0; e < 4; ++e) v[e] = p[min(n + e, N - 1)];
+    }
+    return v;
+}
+
+// y[n .. n+3] of one row: sum * (row scale * channel scale) + bias in fp32, rounded once.
+template <class T, class V>
+__device__ __forceinline__ void put4(T* y, int n, int N, V acc, float s, floatx4 sw, floatx4 bias) {
+    T w[4];
 #pragma unroll
-        for (int i = 0; i < BN * 8 / 256; ++i) {
-            const int at = i * 256 + threadIdx.x, r = at >> 3, c = at & 7;
-            const int64_t n = n0 + r < t.N ? n0 + r : t.N - 1;
-            *reinterpret_cast<i32x4*>(sw + lds_at(r, c)) = load16(t.w + n * t.K, k0 + c * 16, t.K);
-        }
-        __syncthreads();
-        i32x4 b[WM / 16][2];
+    for (int e = 0; e < 4; ++e) w[e] = static_cast<T>(static_cast<float>(acc[e]) * (s * sw[e]) + bias[e]);
+    if (n + 4 <= N) {
+        __builtin_memcpy(y + n, w, sizeof(w));
+    } else {
 #pragma unroll
-        for (int i = 0; i < WM / 16; ++i)
+        for (int e = 0; e < 4; ++e)
+            if (n + e < N) y[n + e] = w[e];
+    }
+}
+
+// f(pointer of y's type)
+template <class F>
+__device__ __forceinline__ void by_type(const A8Task& t, F f) {
+    if (t.y_dtype == RTQ_F32) f(static_cast<float*>(t.y));
+    else if (t.y_dtype == RTQ_F16) f(static_cast<_Float16*>(t.y));
+    else f(static_cast<__bf16*>(t.y));
+}
+
+// ---- few rows: weights straight to registers, K split over the waves ----
+//
+// A workgroup of W waves owns 16 n and 16 MT m. Each wave takes every W-th
+// 128 of K, reads its operands from global memory into registers (each weight
+// byte once over the whole grid for M <= 16 MT) and the waves' sums meet in
+// LDS, in the order of the waves. Bound by the weight stream.
+template <int KIND, int MT, int W, bool ALIGNED>
+__global__ __launch_bounds__(W * 64) void skinny_kernel(const A8Args args) {
+    typedef typename Acc<KIND>::T V;
+    __shared__ V part[W][MT][64];
+    int tile;
+    const A8Task& t = task_of(args, blockIdx.x, tile);
+    const int tiles_n = (t.N + 15) / 16;
+    const int64_t m0 = static_cast<int64_t>(tile / tiles_n) * (16 * MT);
+    const int n0 = tile % tiles_n * 16;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int r16 = lane & 15, g = lane >> 4;
+    const int K = t.K;
+    // rows past the end repeat the last one; their outputs are not stored
+    const uint8_t* w = t.w + static_cast<int64_t>(min(n0 + r16, t.N - 1)) * K + g * 16;
+    const uint8_t* x[MT];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                b[i][h] = *reinterpret_cast<const i32x4*>(sx + lds_at(wm + i * 16 + r16, g + 4 * h));
+    for (int i = 0; i < MT; ++i) {
+        const int64_t m = m0 + i * 16 + r16;
+        x[i] = t.x + (m < args.M ? m : args.M - 1) * K + g * 16;
+    }
+    V acc[MT] = {};
+    int k = wave * kBK;
+    for (; k + kBK <= K; k += W * kBK) {
+        i32x4 a0, a1;
+        __builtin_memcpy(&a0, w + k, 16);
+        __builtin_memcpy(&a1, w + k + 64, 16);
 #pragma unroll
-        for (int i = 0; i < WN / 16; ++i) {
-            i32x4 a[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                a[h] = *reinterpret_cast<const i32x4*>(sw + lds_at(wn + i * 16 + r16, g + 4 * h));
-#pragma unroll
-            for (int q = 0; q < WM / 16; ++q) acc[i][q] = mma<KIND>(a[0], a[1], b[q][0], b[q][1], acc[i][q]);
+        for (int i = 0; i < MT; ++i) {
+            i32x4 b0, b1;
+            __builtin_memcpy(&b0, x[i] + k, 16);
+            __builtin_memcpy(&b1, x[i] + k + 64, 16);
+            acc[i] = mma<KIND>(a0, a1, b0, b1, acc[i]);
         }
     }
-
-    // Lane: column m = lane % 16, rows n = 4 (lane / 16) .. + 3 of each block.
+    if (k < K) {                                               // the last, partial step
+        const int left = K - g * 16;
+        const i32x4 a0 = load16<ALIGNED>(w, k, left), a1 = load16<ALIGNED>(w, k + 64, left);
 #pragma unroll
-    for (int q = 0; q < WM / 16; ++q) {
-        const int64_t m = m0 + wm + q * 16 + r16;
-        if (m >= args.M) continue;
-        const float s = t.x_scale[m];
+        for (int i = 0; i < MT; ++i)
+            acc[i] = mma<KIND>(a0, a1, load16<ALIGNED>(x[i], k, left), load16<ALIGNED>(x[i], k + 64, left), acc[i]);
+    }
 #pragma unroll
-        for (int i = 0; i < WN / 16; ++i) {
-            const int64_t n = n0 + wn + i * 16 + g * 4;
-            if (n >= t.N) continue;
-            float v[4];
+    for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
+    __syncthreads();
+    for (int q = threadIdx.x; q < MT * 64; q += W * 64) {
+        const int i = q >> 6;
+        V sum = part[0][i][lane];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int64_t at = n + e < t.N ? n + e : t.N - 1;
-                const float f = t.w_scale ? s * t.w_scale[at] : s;
-                v[e] = static_cast<float>(acc[i][q][e]) * f;
-                if (t.bias) v[e] += t.bias[at];
-            }
-            store4(t, m, n, v);
+        for (int v = 1; v < W; ++v) sum += part[v][i][lane];
+        const int64_t m = m0 + i * 16 + r16;
+        const int n = n0 + g * 4;
+        if (m < args.M && n < t.N) {
+            const floatx4 sw = channels(t.w_scale, n, t.N, 1.0f), bias = channels(t.bias, n, t.N, 0.0f);
+            by_type(t, [&](auto* y) { put4(y + m * t.ldy, n, t.N, sum, t.x_scale[m], sw, bias); });
         }
     }
 }
 
-template <int KIND, int BM, int BN>
-hipError_t launch_tiles(A8Args& args, hipStream_t stream) {
+// ---- tiles through LDS ----
+
+// LDS: rows of 128 bytes, the 16-byte chunk c of row r at slot c ^ (r & 7):
+// the 16 rows of an operand read hit every bank group evenly.
+__device__ __forceinline__ int lds_at(int r, int c) { return r * kBK + ((c ^ (r & 7)) << 4); }
+
+__device__ const uint32_t zero_chunk[4] = {0, 0, 0, 0};
+
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x70 | 0xf00);
+}
+
+__device__ __forceinline__ void dma16(const uint8_t* src, uint8_t* lds_base) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                     (__attribute__((address_space(3))) void*)lds_base, 16, 0, 0);
+}
+
+// BM x BN outputs by WM x WN waves, stages of 128 of K in two LDS buffers: a
+// stage is copied (DMA to LDS, or through registers where rows are not
+// 16-byte aligned) while the one before it is multiplied.
+template <int KIND, int BM, int BN, int WM, int WN, bool ALIGNED>
+__global__ __launch_bounds__(WM * WN * 64) void tile_kernel(const A8Args args) {
+    constexpr int NW = WM * WN, ROWS = BM + BN;
+    constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
+    constexpr int OPS = ROWS / 8 / NW;                         // 1 KB copies of 8 rows, per wave and stage
+    static_assert(ROWS % (8 * NW) == 0 && BM % (8 * NW) == 0, "copies divide over the waves");
+    __shared__ __align__(1024) uint8_t lds[2][ROWS * kBK];     // rows 0 .. BM-1: x, then the weights
+    int tile;
+    const A8Task& t = task_of(args, blockIdx.x, tile);
+    const int K = t.K;
+    const int tiles_n = (t.N + BN - 1) / BN;
+    const int64_t m0 = static_cast<int64_t>(tile / tiles_n) * BM;
+    const int n0 = tile % tiles_n * BN;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wm = wave % WM * (TM * 16), wn = wave / WM * (TN * 16);
+    const int r16 = lane & 15, g = lane >> 4;
+    const uint8_t* xb = t.x + m0 * K;
+    const uint8_t* wb = t.w + static_cast<int64_t>(n0) * K;
+
+    // Copy j of this wave: rows 8 (j NW + wave) .. + 7, lane: row lane / 8, slot lane % 8.
+    const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;         // (8 j + lane / 8) & 7 = lane / 8
+    uint32_t off[OPS];
+#pragma unroll
+    for (int j = 0; j < OPS; ++j) {
+        const int r = 8 * (j * NW + wave) + (lane >> 3);
+        // rows past the end repeat the last one; their outputs are not stored
+        const int64_t left = r < BM ? args.M - 1 - m0 : static_cast<int64_t>(t.N) - 1 - n0;
+        const int row = r < BM ? r : r - BM;
+        off[j] = static_cast<uint32_t>(row < left ? row : static_cast<int>(left)) * static_cast<uint32_t>(K);
+    }
+    i32x4 hold[ALIGNED ? 1 : OPS];
+    auto issue = [&](int k0, int buf) {
+#pragma unroll
+        for (int j = 0; j < OPS; ++j) {
+            const uint8_t* base = j * NW * 8 < BM ? xb : wb;
+            if constexpr (ALIGNED) {
+                const uint8_t* src = base + k0 + (off[j] + chunk);
+                if (k0 + kBK > K && k0 + chunk >= K) src = reinterpret_cast<const uint8_t*>(zero_chunk);
+                dma16(src, &lds[buf][(j * NW + wave) * 1024]);
+            } else {
+                hold[j] = load16<false>(base + off[j], k0 + chunk, K);
+            }
+        }
+    };
+    auto settle = [&](int buf) {
+        if constexpr (!ALIGNED) {
+#pragma unroll
+            for (int j = 0; j < OPS; ++j)
+                *reinterpret_cast<i32x4*>(&lds[buf][(j * NW + wave) * 1024 + lane * 16]) = hold[j];
+        }
+    };
+
+    typename Acc<KIND>::T acc[TN][TM] = {};
+    issue(0, 0);
+    settle(0);
+    for (int k0 = 0, buf = 0; k0 < K; k0 += kBK, buf ^= 1) {
+        if constexpr (ALIGNED) {
+            // Nothing moves past here: the last stage's LDS reads are all
+            // used, so complete, before the barrier that frees their buffer.
+            __builtin_amdgcn_sched_barrier(0);
+            wait_vm<0>();                                      // this wave's part of the stage
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+        } else {
+            __syncthreads();
+        }
+        const bool more = k0 + kBK < K;
+        if (more) issue(k0 + kBK, buf ^ 1);
+        const uint8_t* xs = lds[buf] + wm * kBK;
+        const uint8_t* ws = lds[buf] + (BM + wn) * kBK;
+        i32x4 b[TM][2];
+#pragma unroll
+        for (int q = 0; q < TM; ++q)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) b[q][h] = *reinterpret_cast<const i32x4*>(xs + lds_at(q * 16 + r16, g + 4 * h));
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+            i32x4 a[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) a[h] = *reinterpret_cast<const i32x4*>(ws + lds_at(i * 16 + r16, g + 4 * h));
+#pragma unroll
+            for (int q = 0; q < TM; ++q) acc[i][q] = mma<KIND>(a[0], a[1], b[q][0], b[q][1], acc[i][q]);
+        }
+        if (more) settle(buf ^ 1);
+    }
+
+    // Lane: column m = lane % 16, rows n = 4 (lane / 16) .. + 3 of each block.
+    const int mq = wm + r16, nq = n0 + wn + g * 4;
+    const int M = args.M - m0 < BM ? static_cast<int>(args.M - m0) : BM;     // rows of this tile
+    float sx[TM];
+#pragma unroll
+    for (int q = 0; q < TM; ++q) sx[q] = t.x_scale[m0 + min(mq + q * 16, M - 1)];
+    by_type(t, [&](auto* y) {
+        y += m0 * t.ldy;
+        if (M == BM && n0 + BN <= t.N) {
+#pragma unroll
+            for (int i = 0; i < TN; ++i) {
+                const int n = nq + i * 16;
+                const floatx4 sw = channels(t.w_scale, n, 1 << 30, 1.0f), bias = channels(t.bias, n, 1 << 30, 0.0f);
+#pragma unroll
+                for (int q = 0; q < TM; ++q) put4(y + (mq + q * 16) * t.ldy, n, 1 << 30, acc[i][q], sx[q], sw, bias);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < TN; ++i) {
+                const int n = nq + i * 16;
+                if (n >= t.N) continue;
+                const floatx4 sw = channels(t.w_scale, n, t.N, 1.0f), bias = channels(t.bias, n, t.N, 0.0f);
+#pragma unroll
+                for (int q = 0; q < TM; ++q)
+                    if (mq + q * 16 < M) put4(y + (mq + q * 16) * t.ldy, n, t.N, acc[i][q], sx[q], sw, bias);
+            }
+        }
+    });
+}
+
+// Workgroups of every task of a launch, BM x BN outputs each.
+uint32_t number(A8Args& args, int BM, int BN) {
     int64_t tiles = 0;
     for (int j = 0; j < args.count; ++j) {
         args.begin[j] = static_cast<uint32_t>(tiles);
         tiles += ((args.M + BM - 1) / BM) * ((args.task[j].N + BN - 1) / BN);
     }
-    tile_kernel<KIND, BM, BN><<<static_cast<uint32_t>(tiles), 256, 0, stream>>>(args);
-    return hipGetLastError();
+    return static_cast<uint32_t>(tiles);
+}
+
+template <int KIND, bool ALIGNED>
+hipError_t launch_kind(A8Args& args, hipStream_t stream) {
+    auto skinny = [&](auto mt, auto w) {
+        constexpr int MT = decltype(mt)::value, W = decltype(w)::value;
+        skinny_kernel<KIND, MT, W, ALIGNED><<<number(args, 16 * MT, 16), W * 64, 0, stream>>>(args);
+        return hipGetLastError();
+    };
+    auto tiles = [&](auto bm, auto bn, auto wm, auto wn) {
+        constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value;
+        constexpr int WM = decltype(wm)::value, WN = decltype(wn)::value;
+        tile_kernel<KIND, BM, BN, WM, WN, ALIGNED><<<number(args, BM, BN), WM * WN * 64, 0, stream>>>(args);
+        return hipGetLastError();
+    };
+    using std::integral_constant;
+    if (args.M <= 16) return skinny(integral_constant<int, 1>(), integral_constant<int, 8>());
+    if (args.M <= 128) return skinny(integral_constant<int, 2>(), integral_constant<int, 4>());
+    if (number(args, 128, 128) < 512)
+        return tiles(integral_constant<int, 64>(), integral_constant<int, 64>(), integral_constant<int, 2>(),
+                     integral_constant<int, 2>());
+    if (number(args, 256, 256) < 512)
+        return tiles(integral_constant<int, 128>(), integral_constant<int, 128>(), integral_constant<int, 2>(),
+                     integral_constant<int, 2>());
+    return tiles(integral_constant<int, 256>(), integral_constant<int, 256>(), integral_constant<int, 4>(),
+                 integral_constant<int, 2>());
+}
+
+bool task_aligned(const A8Task& t) {
+    return t.K % 16 == 0 && ((reinterpret_cast<uintptr_t>(t.x) | reinterpret_cast<uintptr_t>(t.w)) & 15) == 0;
 }
 
 }  // namespace
@@ -195,18 +378,21 @@ hipError_t launch_a8(const A8Task* tasks, int count, int64_t M, hipStream_t stre
     // holds fewer than 2^32 threads).
     constexpr int64_t kMaxTiles = int64_t(1) << 23;
     A8Args args;
-    for (int kind = 0; kind < kA8Kinds; ++kind) {
+    // One launch holds tasks of one kind, and of one of the two ways to load.
+    for (int pass = 0; pass < kA8Kinds * 2; ++pass) {
+        const int kind = pass / 2;
+        const bool whole = pass % 2 == 0;
         for (int at = 0; at < count;) {
             int64_t tiles_n = 0;
             const A8Task* slot[kA8Slots];
             args.count = 0;
             for (; at < count && args.count < kA8Slots; ++at) {
-                if (tasks[at].kind != kind) continue;
+                if (tasks[at].kind != kind || task_aligned(tasks[at]) != whole) continue;
                 slot[args.count++] = &tasks[at];
-                tiles_n += (tasks[at].N + 63) / 64;
+                tiles_n += (tasks[at].N + 15) / 16;
             }
             if (!args.count) break;
-            const int64_t most = kMaxTiles / tiles_n > 0 ? kMaxTiles / tiles_n * 64 : 64;
+            const int64_t most = kMaxTiles / tiles_n > 0 ? kMaxTiles / tiles_n * 16 : 16;
             for (int64_t m = 0; m < M; m += most) {
                 args.M = M - m < most ? M - m : most;
                 for (int j = 0; j < args.count; ++j) {
@@ -215,9 +401,10 @@ hipError_t launch_a8(const A8Task* tasks, int count, int64_t M, hipStream_t stre
                     t.x_scale += m;
                     t.y = static_cast<uint8_t*>(t.y) + m * t.ldy * (t.y_dtype == RTQ_F32 ? 4 : 2);
                 }
-                const hipError_t e = kind == kA8Int  ? launch_tiles<kA8Int, 64, 64>(args, stream)
-                                     : kind == kA8F8 ? launch_tiles<kA8F8, 64, 64>(args, stream)
-                                                     : launch_tiles<kA8F8Wide, 64, 64>(args, stream);
+                const hipError_t e =
+                    kind == kA8Int  ? (whole ? launch_kind<kA8Int, true>(args, stream) : launch_kind<kA8Int, false>(args, stream))
+                    : kind == kA8F8 ? (whole ? launch_kind<kA8F8, true>(args, stream) : launch_kind<kA8F8, false>(args, stream))
+                                    : (whole ? launch_kind<kA8F8Wide, true>(args, stream) : launch_kind<kA8F8Wide, false>(args, stream));
                 if (e != hipSuccess) return e;
             }
         }
