@@ -8,7 +8,6 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import weight_only_quantized_rtq_amd as rtq  # noqa: E402
-from weight_only_quantized_rtq_amd import a8  # noqa: E402
 
 OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_FORMAT, ERR_HIP, ERR_OVERLAP = range(7)
 A, B, C, D, E = (0x7f0000000000 + (i << 36) for i in range(5))      # device addresses, never dereferenced
@@ -89,12 +88,28 @@ def test_silu_refusals(lib):
     assert silu(lib, fmt=0, scale=None, dtype=1, out_dtype=2) == ERR_FORMAT
 
 
+class ProjA8(ctypes.Structure):
+    """rtq_proj_a8 as the header lays it out."""
+    _fields_ = [("fmt", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("y_dtype", ctypes.c_int32),
+                ("x", ctypes.c_void_p), ("x_scale", ctypes.c_void_p), ("payload", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+                ("bias", ctypes.c_void_p)]
+
+
 def proj(fmt=2, N=64, K=128, y_dtype=0, x=A, sx=B, w=C, sw=B + (1 << 20), y=D, ldy=None, bias=None):
-    return a8._ProjA8(fmt, N, K, y_dtype, x, sx, w, sw, y, N if ldy is None else ldy, bias)
+    return ProjA8(fmt, N, K, y_dtype, x, sx, w, sw, y, N if ldy is None else ldy, bias)
+
+
+def test_binding_packs_the_descriptor():
+    from weight_only_quantized_rtq_amd.a8 import _PROJ_A8
+    d = ProjA8.from_buffer_copy(_PROJ_A8.pack(2, 64, 128, 1, A, B, C, 0, D, 70, E))
+    assert _PROJ_A8.size == ctypes.sizeof(ProjA8)
+    assert (d.fmt, d.N, d.K, d.y_dtype, d.x, d.x_scale, d.payload, d.scale, d.y, d.ldy, d.bias) == (
+        2, 64, 128, 1, A, B, C, None, D, 70, E)
 
 
 def project(lib, *projs, M=4, n=None):
-    arr = (a8._ProjA8 * len(projs))(*projs)
+    arr = (ProjA8 * len(projs))(*projs)
     return lib.rtq_project_a8(arr, len(projs) if n is None else n, M, None)
 
 

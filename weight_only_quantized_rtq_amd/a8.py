@@ -15,7 +15,7 @@ gradients.
 from __future__ import annotations
 
 import contextlib
-import ctypes
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -28,11 +28,8 @@ _FMTS = {None: FMT_NONE, "q8": FMT_Q8, "f8": FMT_F8}
 _CODES = {FMT_Q8: torch.int8, FMT_F8: torch.uint8}
 
 
-class _ProjA8(ctypes.Structure):
-    _fields_ = [("fmt", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("y_dtype", ctypes.c_int32),
-                ("x", ctypes.c_void_p), ("x_scale", ctypes.c_void_p), ("payload", ctypes.c_void_p),
-                ("scale", ctypes.c_void_p), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
-                ("bias", ctypes.c_void_p)]
+# rtq_proj_a8: fmt, N, K, y_dtype, x, x_scale, payload, scale, y, ldy, bias
+_PROJ_A8 = struct.Struct("@iiiiPPPPPqP")
 
 
 @dataclass
@@ -66,19 +63,33 @@ class A8Rows:
         return codes.to(torch.float32) * self.scale[:, None]
 
 
-def _rows(t, name: str, shape=None, dtype=None) -> int:
+def _device_of(t) -> int:
+    """The device of a call: the current one, which every tensor has to be on.
+    What is no device tensor is refused by its own check, without asking for one."""
+    return torch.cuda.current_device() if isinstance(t, torch.Tensor) and t.is_cuda else -2
+
+
+def _plain(t, dtype, name: str, dev: int):
+    """A contiguous device tensor of a type (as _need, which words the refusals)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.get_device() == dev and t.is_contiguous()):
+        _need(t, dtype, name)
+    return t.data_ptr()
+
+
+def _rows(t, name: str, dev: int, shape=None, dtype=None) -> int:
     """Checks a [M, K] tensor whose rows may be strided; returns the row stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in _DTYPES if dtype is None else t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype or 'float32, float16 or bfloat16'}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    if t.dim() != 2 or (shape is not None and t.shape != shape):
-        raise ValueError(f"{name} must be {'[M, K]' if shape is None else list(shape)}, got {list(t.shape)}")
-    M, K = t.shape
+    if t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    have = t.shape
+    if len(have) != 2 or (shape is not None and have != shape):
+        raise ValueError(f"{name} must be {'[M, K]' if shape is None else list(shape)}, got {list(have)}")
+    M, K = have
     ld, step = t.stride()
     if step != 1 and K > 1:
         raise ValueError(f"{name}: the elements of a row must be adjacent, stride {t.stride()}")
@@ -87,6 +98,11 @@ def _rows(t, name: str, shape=None, dtype=None) -> int:
     if ld < K:
         raise ValueError(f"{name}: rows overlap, stride {t.stride()}")
     return ld
+
+
+def _launch_stream(stream, dev: int) -> int:
+    """The raw stream of the call: the device's current one, or the given one."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _on(stream):
@@ -103,7 +119,7 @@ def _fmt(fmt) -> int:
         raise ValueError(f"unknown format {fmt!r}") from None
 
 
-def _row_out(out, M: int, K: int, x, fmt: int, out_dtype, stream):
+def _row_out(out, M: int, K: int, x, fmt: int, out_dtype, stream, dev: int):
     """The output of a row operator, checked or new: (object to return, its
     pointer, the scale's pointer, its dtype code)."""
     if fmt == FMT_NONE:
@@ -113,29 +129,27 @@ def _row_out(out, M: int, K: int, x, fmt: int, out_dtype, stream):
                 raise TypeError(f"out_dtype must be {x.dtype} or float32, got {out_dtype}")
             with _on(stream):
                 out = torch.empty((M, K), dtype=out_dtype, device=x.device)
-        else:
-            if not isinstance(out, torch.Tensor) or out.dtype not in (x.dtype, torch.float32) \
-                    or out_dtype not in (None, out.dtype):
-                raise TypeError(f"out must be a {x.dtype} or float32 tensor (of out_dtype, where that is given)")
-            _need(out, out.dtype, "out")
-            if out.shape != (M, K):
-                raise ValueError(f"out must be [{M}, {K}], got {list(out.shape)}")
-        return out, out.data_ptr(), None, _DTYPES[out.dtype]
+        elif not isinstance(out, torch.Tensor) or out.dtype not in (x.dtype, torch.float32) \
+                or out_dtype not in (None, out.dtype):
+            raise TypeError(f"out must be a {x.dtype} or float32 tensor (of out_dtype, where that is given)")
+        p = _plain(out, out.dtype, "out", dev)
+        if out.shape != (M, K):
+            raise ValueError(f"out must be [{M}, {K}], got {list(out.shape)}")
+        return out, p, None, _DTYPES[out.dtype]
     if out_dtype is not None:
         raise TypeError("out_dtype is for dense output (fmt None)")
     if out is None:
         with _on(stream):
             out = A8Rows(torch.empty((M, K), dtype=_CODES[fmt], device=x.device),
                          torch.empty((M,), dtype=torch.float32, device=x.device))
-    else:
-        if not isinstance(out, A8Rows):
-            raise TypeError("out must be an A8Rows")
-        _need(out.codes, _CODES[fmt], "out.codes")
-        _need(out.scale, torch.float32, "out.scale")
-        if out.codes.shape != (M, K) or out.scale.shape != (M,):
-            raise ValueError(f"out must hold [{M}, {K}] codes and [{M}] scales, got {list(out.codes.shape)} and "
-                             f"{list(out.scale.shape)}")
-    return out, out.codes.data_ptr(), out.scale.data_ptr(), 0
+    elif not isinstance(out, A8Rows):
+        raise TypeError("out must be an A8Rows")
+    codes, scale = out.codes, out.scale
+    p, s = _plain(codes, _CODES[fmt], "out.codes", dev), _plain(scale, torch.float32, "out.scale", dev)
+    if codes.shape != (M, K) or scale.shape != (M,):
+        raise ValueError(f"out must hold [{M}, {K}] codes and [{M}] scales, got {list(codes.shape)} and "
+                         f"{list(scale.shape)}")
+    return out, p, s, 0
 
 
 def quantize_rows(x: torch.Tensor, fmt: str = "q8", out: A8Rows | None = None, stream=None) -> A8Rows:
@@ -144,10 +158,11 @@ def quantize_rows(x: torch.Tensor, fmt: str = "q8", out: A8Rows | None = None, s
     code = _fmt(fmt)
     if code == FMT_NONE:
         raise ValueError('quantize_rows writes "q8" or "f8"')
-    ld = _rows(x, "x")
+    dev = _device_of(x)
+    ld = _rows(x, "x", dev)
     M, K = x.shape
-    out, p, s, _ = _row_out(out, M, K, x, code, None, stream)
-    _check(lib.rtq_quantize_rows(x.data_ptr(), ld, _DTYPES[x.dtype], code, p, s, M, K, _stream(stream)))
+    out, p, s, _ = _row_out(out, M, K, x, code, None, stream, dev)
+    _check(lib.rtq_quantize_rows(x.data_ptr(), ld, _DTYPES[x.dtype], code, p, s, M, K, _launch_stream(stream, dev)))
     return out
 
 
@@ -159,24 +174,27 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual:
     the result is (output, h); sum_out holds h and may be x or residual itself."""
     lib = load_library()
     code = _fmt(fmt)
-    ld = _rows(x, "x")
-    M, K = x.shape
-    _need(weight, torch.float32, "weight")
+    dev = _device_of(x)
+    ld = _rows(x, "x", dev)
+    shape = x.shape
+    M, K = shape
+    wp = _plain(weight, torch.float32, "weight", dev)
     if weight.shape != (K,):
         raise ValueError(f"weight must be [{K}], got {list(weight.shape)}")
+    rp = sp = None
     ldr = lds = 0
     if residual is not None:
-        ldr = _rows(residual, "residual", x.shape, x.dtype)
+        ldr = _rows(residual, "residual", dev, shape, x.dtype)
         if sum_out is None:
             with _on(stream):
-                sum_out = torch.empty((M, K), dtype=x.dtype, device=x.device)
-        lds = _rows(sum_out, "sum_out", x.shape, x.dtype)
+                sum_out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        lds = _rows(sum_out, "sum_out", dev, shape, x.dtype)
+        rp, sp = residual.data_ptr(), sum_out.data_ptr()
     elif sum_out is not None:
         raise ValueError("sum_out needs a residual")
-    out, p, s, out_code = _row_out(out, M, K, x, code, out_dtype, stream)
-    _check(lib.rtq_rms_norm(x.data_ptr(), ld, None if residual is None else residual.data_ptr(), ldr,
-                            None if residual is None else sum_out.data_ptr(), lds, weight.data_ptr(), eps,
-                            _DTYPES[x.dtype], code, out_code, p, s, M, K, _stream(stream)))
+    out, p, s, out_code = _row_out(out, M, K, x, code, out_dtype, stream, dev)
+    _check(lib.rtq_rms_norm(x.data_ptr(), ld, rp, ldr, sp, lds, wp, eps, _DTYPES[x.dtype], code, out_code, p, s, M, K,
+                            _launch_stream(stream, dev)))
     return out if residual is None else (out, sum_out)
 
 
@@ -184,38 +202,44 @@ def silu_mul(a: torch.Tensor, b: torch.Tensor, fmt: str | None = None, out=None,
     """silu(a) * b (rtq_silu_mul): A8Rows for fmt "q8" / "f8", else dense."""
     lib = load_library()
     code = _fmt(fmt)
-    lda = _rows(a, "a")
-    ldb = _rows(b, "b", a.shape, a.dtype)
+    dev = _device_of(a)
+    lda = _rows(a, "a", dev)
+    ldb = _rows(b, "b", dev, a.shape, a.dtype)
     M, K = a.shape
-    out, p, s, out_code = _row_out(out, M, K, a, code, out_dtype, stream)
+    out, p, s, out_code = _row_out(out, M, K, a, code, out_dtype, stream, dev)
     _check(lib.rtq_silu_mul(a.data_ptr(), lda, b.data_ptr(), ldb, _DTYPES[a.dtype], code, out_code, p, s, M, K,
-                            _stream(stream)))
+                            _launch_stream(stream, dev)))
     return out
 
 
-def _pack(d: _ProjA8, x: A8Rows, w, y: torch.Tensor, bias) -> None:
+def _pack(x: A8Rows, w, y: torch.Tensor, bias, dev: int, known: A8Rows | None = None) -> bytes:
+    """One checked descriptor. `known` is rows of this call that are checked already."""
     if not isinstance(x, A8Rows):
         raise TypeError("x must be an A8Rows (quantize_rows, rms_norm or silu_mul with a format)")
     if not isinstance(w, (Q8Weight, F8Weight)):
         raise TypeError(f"8-bit rows multiply a Q8Weight or an F8Weight, got {type(w).__name__}")
-    x.validate()
-    w.validate()
-    if x.fmt != w.fmt:
-        raise TypeError(f"{'int8' if x.fmt == FMT_Q8 else 'E4M3'} rows do not multiply a {type(w).__name__}")
-    if x.K != w.K:
-        raise ValueError(f"x must be [M, {w.K}], got {list(x.codes.shape)}")
-    d.fmt, d.N, d.K = w.fmt, w.N, w.K
-    d.ldy = _rows(y, "y", (x.M, w.N))
-    d.y_dtype = _DTYPES[y.dtype]
-    d.x, d.x_scale = x.codes.data_ptr(), x.scale.data_ptr()
-    d.payload = w.payload.data_ptr()
-    d.scale = w.scale.data_ptr() if w.fmt == FMT_Q8 else None
-    d.y = y.data_ptr()
+    codes, fmt = x.codes, w.fmt
+    if codes.dtype != _CODES[fmt]:
+        raise TypeError(f"{codes.dtype} rows do not multiply a {type(w).__name__}")
+    if x is not known:
+        x.validate()
+    M, K = codes.shape
+    payload = w.payload
+    wp = _plain(payload, _CODES[fmt], "payload", dev)
+    if payload.dim() != 2 or payload.shape[1] != K:
+        raise ValueError(f"x is {list(codes.shape)}, the weight {list(payload.shape)}")
+    N = payload.shape[0]
+    sp = bp = 0
+    if fmt == FMT_Q8:
+        sp = _plain(w.scale, torch.float32, "scale", dev)
+        if w.scale.shape != (N,):
+            raise ValueError(f"int8 weight shapes disagree: payload {list(payload.shape)}, scale {list(w.scale.shape)}")
+    ldy = _rows(y, "y", dev, (M, N))
     if bias is not None:
-        _need(bias, torch.float32, "bias")
-        if bias.shape != (w.N,):
-            raise ValueError(f"bias {list(bias.shape)} does not match N={w.N}")
-        d.bias = bias.data_ptr()
+        bp = _plain(bias, torch.float32, "bias", dev)
+        if bias.shape != (N,):
+            raise ValueError(f"bias {list(bias.shape)} does not match N={N}")
+    return _PROJ_A8.pack(fmt, N, K, _DTYPES[y.dtype], codes.data_ptr(), x.scale.data_ptr(), wp, sp, y.data_ptr(), ldy, bp)
 
 
 def gemm_a8(x: A8Rows, w, y: torch.Tensor | None = None, bias: torch.Tensor | None = None, out_dtype=None,
@@ -233,9 +257,9 @@ def gemm_a8(x: A8Rows, w, y: torch.Tensor | None = None, bias: torch.Tensor | No
             y = torch.empty((x.M, w.N), dtype=out_dtype, device=x.codes.device)
     elif out_dtype not in (None, y.dtype):
         raise TypeError(f"y is {y.dtype}, out_dtype {out_dtype}")
-    d = _ProjA8()
-    _pack(d, x, w, y, bias)
-    _check(lib.rtq_gemm_a8(ctypes.byref(d), x.M, _stream(stream)))
+    dev = _device_of(y)
+    d = _pack(x, w, y, bias, dev)
+    _check(lib.rtq_gemm_a8(d, y.shape[0], _launch_stream(stream, dev)))
     return y
 
 
@@ -246,12 +270,15 @@ def project_a8(projections: list[Projection], stream=None) -> None:
     lib = load_library()
     if not 1 <= len(projections) <= MAX_BLOCKS * 8:
         raise ValueError(f"1..{MAX_BLOCKS * 8} projections per call, got {len(projections)}")
-    arr = (_ProjA8 * len(projections))()
-    for d, p in zip(arr, projections):
-        _pack(d, p.x, p.weight, p.y, p.bias)
-        if p.x.M != projections[0].x.M:
-            raise ValueError(f"the projections of one call share M: {p.x.M} and {projections[0].x.M}")
-    _check(lib.rtq_project_a8(arr, len(arr), projections[0].x.M, _stream(stream)))
+    dev, known, M, packed = _device_of(projections[0].y), None, None, []
+    for p in projections:
+        packed.append(_pack(p.x, p.weight, p.y, p.bias, dev, known))
+        if p.x is not known:
+            known = p.x
+            if M not in (None, known.M):
+                raise ValueError(f"the projections of one call share M: {known.M} and {M}")
+            M = known.M
+    _check(lib.rtq_project_a8(b"".join(packed), len(packed), M, _launch_stream(stream, dev)))
 
 
 def ffn_a8(x: torch.Tensor, weight: torch.Tensor, w1, w3, w2, eps: float = 1e-6,

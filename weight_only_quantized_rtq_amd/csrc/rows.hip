@@ -13,22 +13,25 @@
 //
 // The codes are those of the fp64 formula, as the weight quantizers' are. Two
 // steps make that cheap:
-//  - t = R * p / P is first taken in fp32, whose relative error is below
-//    Src::kDelta. Only where t lies that close to a rounding border (about one
-//    element in 10^4) is the element's p loaded again and the quotient taken
-//    in fp64.
-//  - P itself: exact in fp32 for the quantizer; kept in fp64 for the norm (the
-//    multiply and the maximum run beside the sum of squares); for the gated
+//  - p * (R / P) is taken in fp32 with a factor slightly below and slightly
+//    above R / P, further apart than the relative error Src::kDelta of the
+//    fp32 quotient. Where both round to the same code that is the code;
+//    elsewhere (about one element in 10^4) the element's p is loaded again and
+//    the quotient taken in fp64.
+//  - P itself is exact in fp32 for the quantizer. For the norm and the gated
 //    product the row's candidates, those within 2 * kDelta of the fp32
-//    maximum, are evaluated again in fp64.
+//    maximum, are evaluated again in fp64: one element of most rows.
 // Rows whose P lies outside [2^-60, 2^120], where fp32 products could lose
 // bits to underflow or overflow, and rows with an infinity or a NaN, take
 // every step in fp64.
 //
-// Sums of squares are fp64: no overflow for any finite fp32 row.
+// Sums of squares are fp64 (v_fma_f64 runs at the rate of v_fma_f32 here): no
+// overflow for any finite fp32 row.
 #include <rtq.h>
 
 #include <float.h>
+
+#include <type_traits>
 
 #include "rtq_internal.h"
 
@@ -76,22 +79,18 @@ __device__ __forceinline__ void store_chunk(T* p, int n, const float (&v)[kChunk
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7fffffffu; }
 __device__ __forceinline__ float as_float(uint32_t b) { return __builtin_bit_cast(float, b); }
 
-// ---- sources: fast(k) in fp32, exact(k) in fp64, of one row ----
+// ---- sources: p of one element in fp64 ----
 
 template <class T>
 struct PlainSrc {
-    static constexpr bool kNorm = false, kCandidates = false;
-    // t carries the rounding of R / P and of the product
-    static constexpr float kDelta = 0x1p-21f;
+    static constexpr float kDelta = 0x1p-22f;      // roundings of R / P, of each factor, of the product: 3 * 2^-24
     const T* x;
     __device__ __forceinline__ double exact(int64_t k) const { return static_cast<double>(to_f(x[k])); }
 };
 
 template <class T>
 struct NormSrc {
-    static constexpr bool kNorm = true, kCandidates = false;
-    // the rounding of h * w, of R / P and of the product
-    static constexpr float kDelta = 0x1p-21f;
+    static constexpr float kDelta = 0x1p-21f;      // as above, and the rounding of h * w: 4 * 2^-24
     const T* h;              // the row that is normalised: x, or the stored sum
     const float* w;
     __device__ __forceinline__ double exact(int64_t k) const {
@@ -104,27 +103,29 @@ __device__ __forceinline__ double silu_mul_exact(float a, float b) {
     return d / (1.0 + exp(-d)) * static_cast<double>(b);
 }
 
-// fp32 silu(a) * b. exp(-a) = 2^hi * (1 + lo ln 2) with hi + lo = -a log2 e to
-// about 2^-44, so its relative error is that of v_exp_f32 and two roundings
-// at every a (a single fp32 product would lose |a| * 2^-24). `hard` is set
-// where fp32 cannot hold a factor to full precision (exp overflows, or the
-// sigmoid's product is tiny): that element is taken in fp64.
-__device__ __forceinline__ float silu_mul_fast(float a, float b, bool& hard) {
+// fp32 silu(a) * b = ab / (1 + exp(-a)); ab is returned too. exp(-a) = 2^hi *
+// (1 + lo ln 2) with hi + lo = -a log2 e to about 2^-44, so its relative error
+// is that of v_exp_f32 and two roundings at every a (a single fp32 product
+// would lose |a| * 2^-24). exp stays finite because a is taken as -80 below
+// that: the result is then too large, by less than |ab| * 2^-115 (exp(-80) <
+// 2^-115), which the callers look at. a * b first: it overflows where a
+// factor is huge (the callers see infinity), and where it underflows the
+// result does.
+__device__ __forceinline__ float silu_mul_fast(float a, float b, float& ab) {
     constexpr float kL = -0x1.715476p+0f, kLlo = -0x1.4ae0cp-26f;      // -log2 e, high and low part
-    const float hi = a * kL;
-    const float lo = __builtin_fmaf(a, kLlo, __builtin_fmaf(a, kL, -hi));
+    const float c = __builtin_fmaxf(a, -80.0f);
+    const float hi = c * kL;
+    const float lo = __builtin_fmaf(c, kLlo, __builtin_fmaf(c, kL, -hi));
     const float e0 = __builtin_amdgcn_exp2f(hi);
     const float e = __builtin_fmaf(e0, lo * 0x1.62e43p-1f, e0);
-    const float u = a * __builtin_amdgcn_rcpf(1.0f + e);
-    hard = a < -80.0f || (__builtin_fabsf(u) < 0x1p-100f && a != 0.0f);
-    return u * b;
+    ab = a * b;
+    return ab * __builtin_amdgcn_rcpf(1.0f + e);
 }
 
 template <class T>
 struct SiluSrc {
-    static constexpr bool kNorm = false, kCandidates = true;
-    // v_exp_f32 and v_rcp_f32 (1 ulp each) and six more roundings, twice (in p and in P)
-    static constexpr float kDelta = 0x1p-18f;
+    // v_exp_f32 and v_rcp_f32 (1 ulp each) and four roundings in p, three as the quantizer's: 11 * 2^-24
+    static constexpr float kDelta = 0x1p-20f;
     const T* a;
     const T* b;
     __device__ __forceinline__ double exact(int64_t k) const { return silu_mul_exact(to_f(a[k]), to_f(b[k])); }
@@ -160,34 +161,49 @@ struct CodeOf {
     }
 };
 
-// Codes of eight fp32 values v with factor inv = R / P, packed; bit j of the
-// result's mask: element j is within `delta` of a rounding border.
+// Codes of eight fp32 values v with factors lo < R / P < hi, packed. `differ`:
+// nonzero bytes where the two factors give different codes.
 template <int OUT>
-__device__ __forceinline__ u32x2 fast_codes(const float (&v)[kChunk], float inv, float delta, uint32_t& mask) {
-    u32x2 w = {0u, 0u};
-    mask = 0;
+__device__ __forceinline__ u32x2 fast_codes(const float (&v)[kChunk], float lo, float hi, u32x2& differ) {
+    u32x2 w, d;
     if constexpr (OUT == kOutQ8) {
+        // v * f + 1.5 * 2^23 rounds once, to a whole number, ties to even; its low byte is the code
+        constexpr float kMagic = 12582912.0f;
+        auto pack = [&](int j, float f) {
+            uint32_t r[4];
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) {
-            const float t = v[j] * inv;
-            const float n = __builtin_rintf(t);
-            const float d = __builtin_fabsf(t - n);
-            if (d > __builtin_fmaf(-delta, __builtin_fabsf(t), 0.5f)) mask |= 1u << j;
-            w[j / 4] |= (static_cast<uint32_t>(static_cast<int>(n)) & 0xffu) << (8 * (j % 4));
+            for (int e = 0; e < 4; ++e) r[e] = __builtin_bit_cast(uint32_t, __builtin_fmaf(v[j + e], f, kMagic));
+            const uint32_t a = __builtin_amdgcn_perm(r[1], r[0], 0x0c0c0400u);
+            const uint32_t b = __builtin_amdgcn_perm(r[3], r[2], 0x04000c0cu);
+            return a | b;
+        };
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            w[h] = pack(4 * h, hi);
+            d[h] = w[h] ^ pack(4 * h, lo);
         }
     } else {
+        auto pack = [&](int j, float f) {
+            int r = __builtin_amdgcn_cvt_pk_fp8_f32(v[j] * f, v[j + 1] * f, 0, false);
+            r = __builtin_amdgcn_cvt_pk_fp8_f32(v[j + 2] * f, v[j + 3] * f, r, true);
+            return static_cast<uint32_t>(r);
+        };
 #pragma unroll
-        for (int j = 0; j < kChunk; j += 2) {
-            const float t0 = v[j] * inv, t1 = v[j + 1] * inv;
-            const uint32_t lo = e4m3_pair(t0 * (1.0f - delta), t1 * (1.0f - delta));
-            const uint32_t hi = e4m3_pair(t0 * (1.0f + delta), t1 * (1.0f + delta));
-            const uint32_t x = lo ^ hi;
-            if (x & 0xffu) mask |= 1u << j;
-            if (x & 0xff00u) mask |= 2u << j;
-            w[j / 4] |= hi << (8 * (j % 4));
+        for (int h = 0; h < 2; ++h) {
+            w[h] = pack(4 * h, hi);
+            d[h] = w[h] ^ pack(4 * h, lo);
         }
     }
+    differ = d;
     return w;
+}
+
+// Bit j: byte j is not zero.
+__device__ __forceinline__ uint32_t bytes_set(u32x2 d) {
+    uint32_t mask = 0;
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) mask |= (d[j / 4] >> (8 * (j % 4))) & 0xffu ? 1u << j : 0u;
+    return mask;
 }
 
 __device__ __forceinline__ void store_codes(uint8_t* p, int n, u32x2 w) {
@@ -200,29 +216,59 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int n, u32x2 w) {
     }
 }
 
-// ---- reductions over the TPR threads of a row ----
+// ---- reductions over a wave (DPP: no LDS crossbar), result in every lane ----
 
-template <class V, class F>
-__device__ __forceinline__ V wave_reduce(V v, F f) {
-#pragma unroll
-    for (int s = 32; s >= 1; s >>= 1) v = f(v, __shfl_xor(v, s));
-    return v;
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xf, 0xf, false));
 }
 
-// All threads of the row get the result. `slot` is LDS of TPR / 64 entries of
-// its own for each use within a row.
-template <int TPR, class V, class F>
-__device__ __forceinline__ V row_reduce(V v, V* slot, F f) {
-    v = wave_reduce(v, f);
-    if constexpr (TPR > 64) {
-        constexpr int W = TPR / 64;
-        if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = slot[0];
-#pragma unroll
-        for (int i = 1; i < W; ++i) v = f(v, slot[i]);
+// f(v, CTRL) over row_shr 1, 2, 4, 8, row_bcast 15 and 31: lane 63 ends with
+// the whole wave's. Lanes without a source read 0.
+template <class V, class F>
+__device__ __forceinline__ V wave_scan(V v, F f) {
+    v = f(v, std::integral_constant<int, 0x111>());
+    v = f(v, std::integral_constant<int, 0x112>());
+    v = f(v, std::integral_constant<int, 0x114>());
+    v = f(v, std::integral_constant<int, 0x118>());
+    v = f(v, std::integral_constant<int, 0x142>());
+    return f(v, std::integral_constant<int, 0x143>());
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    v = wave_scan(v, [](uint32_t a, auto c) {
+        const uint32_t b = dpp<decltype(c)::value>(a);
+        return a > b ? a : b;
+    });
+    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
+}
+
+__device__ __forceinline__ double lane_value(double v, int lane) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), lane);
+    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), lane);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+    v = wave_scan(v, [](double a, auto c) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, a);
+        const uint64_t o = static_cast<uint64_t>(dpp<decltype(c)::value>(static_cast<uint32_t>(b >> 32))) << 32 |
+                           dpp<decltype(c)::value>(static_cast<uint32_t>(b));
+        return a + __builtin_bit_cast(double, o);
+    });
+    return lane_value(v, 63);
+}
+
+// The largest of a value that few lanes hold (zero in the others).
+__device__ __forceinline__ double wave_max_sparse(double v) {
+    double best = 0.0;
+    uint64_t lanes = __builtin_amdgcn_ballot_w64(v > 0.0);
+    while (lanes) {
+        best = __builtin_fmax(best, lane_value(v, __builtin_ctzll(lanes)));
+        lanes &= lanes - 1;
     }
-    return v;
+    return best;
 }
 
 struct RowArgs {
@@ -237,26 +283,17 @@ struct RowArgs {
     float eps;
 };
 
-struct Max32 {
-    __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return a > b ? a : b; }
-};
-struct Max64 {
-    __device__ __forceinline__ double operator()(double a, double b) const { return __builtin_fmax(a, b); }
-};
-struct Add64 {
-    __device__ __forceinline__ double operator()(double a, double b) const { return a + b; }
-};
-
+// Sources of rows. first(): the chunk's values in fp32, zeros past n: x, or h
+// (the norm), or p (the gated product; `top_ab` collects max |ab|).
 template <class T>
 struct PlainOp {
     typedef PlainSrc<T> Src;
-    typedef T In;
+    static constexpr bool kNorm = false, kSilu = false;
     static __device__ __forceinline__ Src src(const RowArgs& a, int64_t row) {
         return Src{static_cast<const T*>(a.x) + row * a.ldx};
     }
-    // The chunk's p in fp32 (zeros past n) and, for the norm, h itself.
     static __device__ __forceinline__ void first(const RowArgs& a, int64_t row, int64_t k, int n, float (&p)[kChunk],
-                                                 float (&)[kChunk]) {
+                                                 uint32_t&) {
         load_chunk(static_cast<const T*>(a.x) + row * a.ldx + k, n, p);
     }
 };
@@ -264,7 +301,7 @@ struct PlainOp {
 template <class T>
 struct NormOp {
     typedef NormSrc<T> Src;
-    typedef T In;
+    static constexpr bool kNorm = true, kSilu = false;
     static __device__ __forceinline__ Src src(const RowArgs& a, int64_t row) {
         return a.r ? Src{static_cast<const T*>(a.sum) + row * a.lds, a.weight}
                    : Src{static_cast<const T*>(a.x) + row * a.ldx, a.weight};
@@ -272,9 +309,8 @@ struct NormOp {
     // h = x + residual in fp32, rounded once to the stream's type: what is
     // stored is what is normalised.
     static __device__ __forceinline__ void first(const RowArgs& a, int64_t row, int64_t k, int n, float (&h)[kChunk],
-                                                 float (&w)[kChunk]) {
+                                                 uint32_t&) {
         load_chunk(static_cast<const T*>(a.x) + row * a.ldx + k, n, h);
-        load_chunk(a.weight + k, n, w);
         if (a.r) {
             float r[kChunk];
             load_chunk(static_cast<const T*>(a.r) + row * a.ldr + k, n, r);
@@ -288,22 +324,37 @@ struct NormOp {
 template <class T>
 struct SiluOp {
     typedef SiluSrc<T> Src;
-    typedef T In;
+    static constexpr bool kNorm = false, kSilu = true;
     static __device__ __forceinline__ Src src(const RowArgs& a, int64_t row) {
         return Src{static_cast<const T*>(a.x) + row * a.ldx, static_cast<const T*>(a.r) + row * a.ldr};
     }
     static __device__ __forceinline__ void first(const RowArgs& a, int64_t row, int64_t k, int n, float (&p)[kChunk],
-                                                 float (&)[kChunk]) {
+                                                 uint32_t& top_ab) {
         float b[kChunk];
         load_chunk(static_cast<const T*>(a.x) + row * a.ldx + k, n, p);
         load_chunk(static_cast<const T*>(a.r) + row * a.ldr + k, n, b);
-uint32_t mask = 0;
 #pragma unroll
         for (int j = 0; j < kChunk; ++j) {
-            bool hard;
-            p[j] = silu_mul_fast(p[j], b[j], hard);
-            mask |= hard ? 1u << j : 0u;
+            float ab;
+            p[j] = silu_mul_fast(p[j], b[j], ab);
+            top_ab = max(top_ab, abs_bits(ab));
         }
+    }
+    // Dense rows have no maximum to hide behind: gates below -80 and products
+    // that overflow before the sigmoid are taken in fp64.
+    static __device__ __forceinline__ void dense(const RowArgs& a, int64_t row, int64_t k, int n, float (&p)[kChunk]) {
+        float b[kChunk];
+        uint32_t mask = 0;
+        load_chunk(static_cast<const T*>(a.x) + row * a.ldx + k, n, p);
+        load_chunk(static_cast<const T*>(a.r) + row * a.ldr + k, n, b);
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) {
+            float ab;
+            const bool low = p[j] < -80.0f;
+            p[j] = silu_mul_fast(p[j], b[j], ab);
+            mask |= low || __builtin_fabsf(ab) > FLT_MAX ? 1u << j : 0u;
+        }
+        mask &= n >= kChunk ? 0xffu : (1u << n) - 1u;
         const Src s = src(a, row);
         while (mask) {
             const int h = __builtin_ctz(mask);
@@ -317,199 +368,227 @@ uint32_t mask = 0;
 
 // One row per TPR threads (64: four rows per workgroup of 256; else one), NV
 // chunks of eight elements per thread held in registers: one pass over the
-// data. NV = 0: rows of any length, read a second time for the codes.
+// data. NV = 0: rows of any length, read again for each step. Workgroups take
+// rows in turn; the norm's weight stays in registers across them.
 template <class Op, int OUT, class OutT, int TPR, int NV>
 __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void row_kernel(RowArgs a) {
     constexpr int RPB = TPR == 64 ? 4 : 1;
-    constexpr bool kNorm = Op::Src::kNorm;
+    constexpr bool kNorm = Op::kNorm, kDense = OUT == kOutDense;
+    constexpr bool kReduced = kNorm || !kDense;                // whether a row is reduced at all
     constexpr int W = TPR / 64;
-    __shared__ double sh_d[3][W];
-    __shared__ uint32_t sh_u[W];
+    // By the row's parity: a row's slots are written again two rows later,
+    // behind the barrier of the row between.
+    __shared__ double sh_ss[2][W], sh_best[2][W];
+    __shared__ uint32_t sh_top[2][W], sh_ab[2][W];
     const int lane = TPR == 64 ? static_cast<int>(threadIdx.x & 63) : static_cast<int>(threadIdx.x);
-    const int chunks = static_cast<int>((a.K + kChunk - 1) / kChunk);
-    const int per = NV > 0 ? NV : (chunks + TPR - 1) / TPR;
+    const int wave = threadIdx.x >> 6;
+    const int per = NV > 0 ? NV : static_cast<int>((a.K + kChunk * TPR - 1) / (kChunk * TPR));
+    auto chunk_k = [&](int i) { return static_cast<int64_t>(i * TPR + lane) * kChunk; };
+    auto chunk_n = [&](int64_t k) { return static_cast<int>(a.K - k < kChunk ? a.K - k : kChunk); };   // <= 0: none
 
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * RPB + (TPR == 64 ? threadIdx.x >> 6 : 0); row < a.M;
-         row += static_cast<int64_t>(gridDim.x) * RPB) {
-        float keep[NV > 0 ? NV : 1][kChunk];
-        float keep_w[NV > 0 && kNorm ? NV : 1][kChunk];
-        uint32_t top = 0;
-        double top_d = 0.0, ss = 0.0;
+    float w[kNorm && NV > 0 ? NV : 1][kChunk];
+    if constexpr (kNorm && NV > 0) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) load_chunk(a.weight + chunk_k(i), chunk_n(chunk_k(i)), w[i]);
+    }
 
-        auto chunk_n = [&](int i) { return static_cast<int64_t>(i * TPR + lane) * kChunk; };
-        auto take = [&](int i, float (&v)[kChunk], float (&w)[kChunk]) {
-            const int64_t k = chunk_n(i);
-            const int n = k < a.K ? static_cast<int>(a.K - k < kChunk ? a.K - k : kChunk) : 0;
+    int parity = 0;
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * RPB + (TPR == 64 ? wave : 0); row < a.M;
+         row += static_cast<int64_t>(gridDim.x) * RPB, parity ^= 1) {
+        const typename Op::Src src = Op::src(a, row);
+        float v[NV > 0 ? NV : 1][kChunk];
+        uint32_t top = 0, top_ab = 0;
+        double ss = 0.0;
+
+        auto take = [&](int i, float (&x)[kChunk]) {
+            const int64_t k = chunk_k(i);
+            const int n = chunk_n(k);
             if (n > 0) {
-                Op::first(a, row, k, n, v, w);
+                if constexpr (Op::kSilu && kDense) Op::dense(a, row, k, n, x);
+                else Op::first(a, row, k, n, x, top_ab);
             } else {
 #pragma unroll
-                for (int j = 0; j < kChunk; ++j) v[j] = w[j] = 0.0f;
+                for (int j = 0; j < kChunk; ++j) x[j] = 0.0f;
             }
         };
-        auto look = [&](float (&v)[kChunk], const float (&w)[kChunk]) {
+        // The same values once more, of a row that first() has been through.
+        auto again = [&](int i, float (&x)[kChunk]) {
+            if constexpr (kNorm) {
+                const int64_t k = chunk_k(i);
+                load_chunk(src.h + k, chunk_n(k), x);
+                load_chunk(src.w + k, chunk_n(k), w[0]);
+            } else {
+                take(i, x);
+            }
+        };
+        auto look = [&](const float (&x)[kChunk], const float (&wx)[kChunk]) {
 #pragma unroll
             for (int j = 0; j < kChunk; ++j) {
                 if constexpr (kNorm) {
-                    const double h = v[j];
+                    const double h = x[j];
                     ss = __builtin_fma(h, h, ss);
-                    if constexpr (OUT != kOutDense) {
-                        top_d = __builtin_fmax(top_d, __builtin_fabs(h * static_cast<double>(w[j])));
-                        top = Max32()(top, abs_bits(v[j] * w[j]));
-                    }
-                } else if constexpr (OUT != kOutDense) {
-                    top = Max32()(top, abs_bits(v[j]));
                 }
+                if constexpr (!kDense) top = max(top, abs_bits(kNorm ? x[j] * wx[j] : x[j]));
             }
         };
         if constexpr (NV > 0) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) take(i, keep[i], keep_w[kNorm ? i : 0]);
+            for (int i = 0; i < NV; ++i) take(i, v[i]);
+            if constexpr (kReduced) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) look(keep[i], keep_w[kNorm ? i : 0]);
-        } else {
+                for (int i = 0; i < NV; ++i) look(v[i], w[kNorm ? i : 0]);
+            }
+        } else if constexpr (kReduced) {
             for (int i = 0; i < per; ++i) {
-                take(i, keep[0], keep_w[0]);
-                look(keep[0], keep_w[0]);
+                take(i, v[0]);
+                if constexpr (kNorm) load_chunk(src.w + chunk_k(i), chunk_n(chunk_k(i)), w[0]);
+                look(v[0], w[0]);
             }
         }
-        // The row's slots of the last row may still be read.
-        if constexpr (TPR > 64) __syncthreads();
-        double r = 1.0;
-        if constexpr (kNorm) {
-            ss = row_reduce<TPR>(ss, sh_d[0], Add64());
-            r = 1.0 / __builtin_sqrt(ss / static_cast<double>(a.K) + static_cast<double>(a.eps));
+        const uint32_t lane_top = top;
+        if constexpr (kReduced) {
+            if constexpr (kNorm) ss = wave_sum(ss);
+            if constexpr (!kDense) top = wave_max(top);
+            if constexpr (Op::kSilu) top_ab = wave_max(top_ab);
+            if constexpr (TPR > 64) {
+                if ((threadIdx.x & 63) == 0) {
+                    if constexpr (kNorm) sh_ss[parity][wave] = ss;
+                    sh_top[parity][wave] = top;
+                    if constexpr (Op::kSilu) sh_ab[parity][wave] = top_ab;
+                }
+                __syncthreads();
+                ss = 0.0;
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    if constexpr (kNorm) ss += sh_ss[parity][i];
+                    top = max(top, sh_top[parity][i]);
+                    if constexpr (Op::kSilu) top_ab = max(top_ab, sh_ab[parity][i]);
+                }
+            }
         }
+        double r = 1.0;
+        if constexpr (kNorm) r = 1.0 / __builtin_sqrt(ss / static_cast<double>(a.K) + static_cast<double>(a.eps));
 
-        const typename Op::Src src = Op::src(a, row);
-        if constexpr (OUT == kOutDense) {
+        if constexpr (kDense) {
             OutT* out = static_cast<OutT*>(a.out) + row * a.K;
             const float rf = static_cast<float>(r);
-            auto put = [&](int i, float (&v)[kChunk], const float (&w)[kChunk]) {
-                const int64_t k = chunk_n(i);
-                if (k >= a.K) return;
-                const int n = static_cast<int>(a.K - k < kChunk ? a.K - k : kChunk);
+            auto put = [&](int i, float (&x)[kChunk], const float (&wx)[kChunk]) {
+                const int64_t k = chunk_k(i);
+                const int n = chunk_n(k);
+                if (n <= 0) return;
                 if constexpr (kNorm) {
 #pragma unroll
-                    for (int j = 0; j < kChunk; ++j) v[j] = v[j] * rf * w[j];
+                    for (int j = 0; j < kChunk; ++j) x[j] = x[j] * rf * wx[j];
                 }
-                store_chunk(out + k, n, v);
+                store_chunk(out + k, n, x);
             };
             if constexpr (NV > 0) {
 #pragma unroll
-                for (int i = 0; i < NV; ++i) put(i, keep[i], keep_w[kNorm ? i : 0]);
+                for (int i = 0; i < NV; ++i) put(i, v[i], w[kNorm ? i : 0]);
             } else {
                 for (int i = 0; i < per; ++i) {
-                    if constexpr (kNorm) {
-                        const int64_t k = chunk_n(i);
-                        const int n = k < a.K ? static_cast<int>(a.K - k < kChunk ? a.K - k : kChunk) : 0;
-                        load_chunk(src.h + k, n, keep[0]);
-                        load_chunk(src.w + k, n, keep_w[0]);
-                    } else {
-                        take(i, keep[0], keep_w[0]);
-                    }
-                    put(i, keep[0], keep_w[0]);
+                    again(i, v[0]);
+                    put(i, v[0], w[0]);
                 }
             }
         } else {
             typedef CodeOf<OUT> Code;
-            top = row_reduce<TPR>(top, sh_u, Max32());
+            constexpr float kDelta = Op::Src::kDelta;
             const float pf = as_float(top);
-            const bool fast = pf >= 0x1p-60f && pf <= 0x1p120f;      // false for NaN
-            double P;
-            if (fast) {
-                if constexpr (kNorm) {
-                    P = row_reduce<TPR>(top_d, sh_d[1], Max64());
-                } else if constexpr (Op::Src::kCandidates) {
-                    const float near = pf * (1.0f - 2.0f * Op::Src::kDelta);
-                    double best = 0.0;
-                    auto candidates = [&](const float (&v)[kChunk]) {
+            bool fast = pf >= 0x1p-60f && pf <= 0x1p120f;            // false for NaN
+            // the gates below -80: their error stays under 2^-40 of P
+            if constexpr (Op::kSilu) fast = fast && as_float(top_ab) <= pf * 0x1p75f;
+            double P = static_cast<double>(pf);
+            if (kNorm || Op::kSilu || !fast) {
+                const float near = pf * (1.0f - 2.0f * kDelta);
+                double best = 0.0;
+                if (!fast) {
+                    for (int i = 0; i < per; ++i) {
+                        const int64_t k = chunk_k(i);
+                        const int n = chunk_n(k);
+                        for (int j = 0; j < n; ++j) {
+                            const double p = __builtin_fabs(src.exact(k + j));
+                            best = __builtin_fmax(best, p <= DBL_MAX ? p : static_cast<double>(__builtin_inff()));
+                        }
+                    }
+                } else if (as_float(lane_top) >= near) {
+                    auto candidates = [&](const float (&x)[kChunk], const float (&wx)[kChunk]) {
                         uint32_t mask = 0;
 #pragma unroll
-                        for (int j = 0; j < kChunk; ++j) mask |= __builtin_fabsf(v[j]) >= near ? 1u << j : 0u;
+                        for (int j = 0; j < kChunk; ++j)
+                            mask |= __builtin_fabsf(kNorm ? x[j] * wx[j] : x[j]) >= near ? 1u << j : 0u;
                         return mask;
                     };
                     auto settle = [&](int i0, uint32_t mask) {
                         while (mask) {
                             const int b = __builtin_ctz(mask);
                             mask &= mask - 1u;
-                            best = __builtin_fmax(best, __builtin_fabs(src.exact(chunk_n(i0 + b / kChunk) + b % kChunk)));
+                            best = __builtin_fmax(best, __builtin_fabs(src.exact(chunk_k(i0 + b / kChunk) + b % kChunk)));
                         }
                     };
                     if constexpr (NV > 0) {
                         uint32_t mask = 0;
 #pragma unroll
-                        for (int i = 0; i < NV; ++i) mask |= candidates(keep[i]) << (kChunk * i);
+                        for (int i = 0; i < NV; ++i) mask |= candidates(v[i], w[kNorm ? i : 0]) << (kChunk * i);
                         settle(0, mask);
                     } else {
                         for (int i = 0; i < per; ++i) {
-                            take(i, keep[0], keep_w[0]);
-                            settle(i, candidates(keep[0]));
+                            again(i, v[0]);
+                            settle(i, candidates(v[0], w[0]));
                         }
                     }
-                    P = row_reduce<TPR>(best, sh_d[1], Max64());
-                } else {
-                    P = static_cast<double>(pf);
                 }
-            } else {
-                double best = 0.0;
-                for (int i = 0; i < per; ++i) {
-                    const int64_t k = chunk_n(i);
-                    for (int j = 0; j < kChunk; ++j) {
-                        if (k + j >= a.K) continue;
-                        const double p = __builtin_fabs(src.exact(k + j));
-                        best = __builtin_fmax(best, p <= DBL_MAX ? p : static_cast<double>(__builtin_inff()));
-                    }
+                P = wave_max_sparse(best);
+                if constexpr (TPR > 64) {
+                    if ((threadIdx.x & 63) == 0) sh_best[parity][wave] = P;
+                    __syncthreads();
+#pragma unroll
+                    for (int i = 0; i < W; ++i) P = __builtin_fmax(P, sh_best[parity][i]);
                 }
-                P = row_reduce<TPR>(best, sh_d[1], Max64());
             }
             const float scale = static_cast<float>(P * r / static_cast<double>(Code::kTop));
             const bool fine = scale <= FLT_MAX;                      // false for NaN and infinity
             if (lane == 0) a.scale[row] = fine ? scale : __builtin_nanf("");
             uint8_t* out = static_cast<uint8_t*>(a.out) + row * a.K;
-            const bool zero = !fine || P == 0.0;
+            const bool zero = !fine || P == 0.0, quick = fast && fine;
             const float inv = static_cast<float>(static_cast<double>(Code::kTop) / P);
+            const float lo = inv * (1.0f - kDelta), hi = inv * (1.0f + kDelta);
             // Stores the codes of chunk i; returns the elements still to be taken in fp64.
-            auto put = [&](int i, const float (&v)[kChunk], const float (&w)[kChunk]) {
-                const int64_t k = chunk_n(i);
-                if (k >= a.K) return 0u;
-                const int n = static_cast<int>(a.K - k < kChunk ? a.K - k : kChunk);
+            auto put = [&](int i, const float (&x)[kChunk], const float (&wx)[kChunk]) {
+                const int64_t k = chunk_k(i);
+                const int n = chunk_n(k);
+                if (n <= 0) return 0u;
                 u32x2 c = {0u, 0u};
                 uint32_t mask = zero ? 0u : 0xffu;
-                if (fast && fine) {
+                if (quick) {
                     float p[kChunk];
 #pragma unroll
-                    for (int j = 0; j < kChunk; ++j) p[j] = kNorm ? v[j] * w[j] : v[j];
-                    c = fast_codes<OUT>(p, inv, Op::Src::kDelta, mask);
+                    for (int j = 0; j < kChunk; ++j) p[j] = kNorm ? x[j] * wx[j] : x[j];
+                    u32x2 d;
+                    c = fast_codes<OUT>(p, lo, hi, d);
+                    mask = d[0] | d[1] ? bytes_set(d) : 0u;
                 }
                 store_codes(out + k, n, c);
-                return mask & ((1u << n) - 1u);
+                return n >= kChunk ? mask : mask & ((1u << n) - 1u);
             };
             // The same thread stored these elements' chunk, so the bytes land in this order.
             auto settle = [&](int i0, uint32_t mask) {
                 while (mask) {
                     const int b = __builtin_ctz(mask);
                     mask &= mask - 1u;
-                    const int64_t k = chunk_n(i0 + b / kChunk) + b % kChunk;
+                    const int64_t k = chunk_k(i0 + b / kChunk) + b % kChunk;
                     out[k] = static_cast<uint8_t>(Code::exact(src.exact(k), P));
                 }
             };
             if constexpr (NV > 0) {
                 uint32_t mask = 0;
 #pragma unroll
-                for (int i = 0; i < NV; ++i) mask |= put(i, keep[i], keep_w[kNorm ? i : 0]) << (kChunk * i);
+                for (int i = 0; i < NV; ++i) mask |= put(i, v[i], w[kNorm ? i : 0]) << (kChunk * i);
                 settle(0, mask);
             } else {
                 for (int i = 0; i < per; ++i) {
-                    if constexpr (kNorm) {
-                        const int64_t k = chunk_n(i);
-                        const int n = k < a.K ? static_cast<int>(a.K - k < kChunk ? a.K - k : kChunk) : 0;
-                        load_chunk(src.h + k, n, keep[0]);
-                        load_chunk(src.w + k, n, keep_w[0]);
-                    } else {
-                        take(i, keep[0], keep_w[0]);
-                    }
-                    settle(i, put(i, keep[0], keep_w[0]));
+                    again(i, v[0]);
+                    settle(i, put(i, v[0], w[0]));
                 }
             }
         }
