@@ -47,20 +47,26 @@ __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(_Float16 v) { return static_cast<float>(v); }
 __device__ __forceinline__ float to_f(__bf16 v) { return static_cast<float>(v); }
 
-// Loads and stores of a whole chunk go through memcpy: one 16-byte access per
-// 16 bytes at any alignment of the row.
+// A chunk as it lies in memory. Loads are kept apart from the conversions, so
+// that a thread's loads are all in flight before the first is waited for; a
+// whole chunk goes through memcpy: one 16-byte access per 16 bytes at any
+// alignment of the row. Zeros past n (n <= 0: no element).
 template <class T>
-__device__ __forceinline__ void load_chunk(const T* p, int n, float (&v)[kChunk]) {
-    if (n >= kChunk) {
-        T t[kChunk];
-        __builtin_memcpy(t, p, sizeof(t));
+struct Raw {
+    T t[kChunk];
+    __device__ __forceinline__ void load(const T* p, int n) {
+        if (n >= kChunk) {
+            __builtin_memcpy(t, p, sizeof(t));
+        } else {
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j) t[j] = j < n ? p[j] : static_cast<T>(0.0f);
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[kChunk]) const {
 #pragma unroll
         for (int j = 0; j < kChunk; ++j) v[j] = to_f(t[j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j) v[j] = j < n ? to_f(p[j]) : 0.0f;
     }
-}
+};
 
 template <class T>
 __device__ __forceinline__ void store_chunk(T* p, int n, const float (&v)[kChunk]) {
@@ -283,18 +289,22 @@ struct RowArgs {
     float eps;
 };
 
-// Sources of rows. first(): the chunk's values in fp32, zeros past n: x, or h
-// (the norm), or p (the gated product; `top_ab` collects max |ab|).
+// Sources of rows. load(): a chunk of the inputs; values(): what is kept of it
+// in fp32: x, or h (the norm, which stores it), or p (the gated product;
+// `top_ab` collects max |ab|).
 template <class T>
 struct PlainOp {
     typedef PlainSrc<T> Src;
     static constexpr bool kNorm = false, kSilu = false;
+    Raw<T> x;
     static __device__ __forceinline__ Src src(const RowArgs& a, int64_t row) {
         return Src{static_cast<const T*>(a.x) + row * a.ldx};
     }
-    static __device__ __forceinline__ void first(const RowArgs& a, int64_t row, int64_t k, int n, float (&p)[kChunk],
-                                                 uint32_t&) {
-        load_chunk(static_cast<const T*>(a.x) + row * a.ldx + k, n, p);
+    __device__ __forceinline__ void load(const RowArgs& a, int64_t row, int64_t k, int n) {
+        x.load(static_cast<const T*>(a.x) + row * a.ldx + k, n);
+    }
+    __device__ __forceinline__ void values(const RowArgs&, int64_t, int64_t, int, float (&p)[kChunk], uint32_t&) {
+        x.get(p);
     }
 };
 
@@ -302,20 +312,24 @@ template <class T>
 struct NormOp {
     typedef NormSrc<T> Src;
     static constexpr bool kNorm = true, kSilu = false;
+    Raw<T> x, r;
     static __device__ __forceinline__ Src src(const RowArgs& a, int64_t row) {
         return a.r ? Src{static_cast<const T*>(a.sum) + row * a.lds, a.weight}
                    : Src{static_cast<const T*>(a.x) + row * a.ldx, a.weight};
     }
+    __device__ __forceinline__ void load(const RowArgs& a, int64_t row, int64_t k, int n) {
+        x.load(static_cast<const T*>(a.x) + row * a.ldx + k, n);
+        if (a.r) r.load(static_cast<const T*>(a.r) + row * a.ldr + k, n);
+    }
     // h = x + residual in fp32, rounded once to the stream's type: what is
     // stored is what is normalised.
-    static __device__ __forceinline__ void first(const RowArgs& a, int64_t row, int64_t k, int n, float (&h)[kChunk],
-                                                 uint32_t&) {
-        load_chunk(static_cast<const T*>(a.x) + row * a.ldx + k, n, h);
+    __device__ __forceinline__ void values(const RowArgs& a, int64_t row, int64_t k, int n, float (&h)[kChunk], uint32_t&) {
+        x.get(h);
         if (a.r) {
-            float r[kChunk];
-            load_chunk(static_cast<const T*>(a.r) + row * a.ldr + k, n, r);
+            float b[kChunk];
+            r.get(b);
 #pragma unroll
-            for (int j = 0; j < kChunk; ++j) h[j] = to_f(static_cast<T>(h[j] + r[j]));
+            for (int j = 0; j < kChunk; ++j) h[j] = to_f(static_cast<T>(h[j] + b[j]));
             store_chunk(static_cast<T*>(a.sum) + row * a.lds + k, n, h);
         }
     }
@@ -325,14 +339,18 @@ template <class T>
 struct SiluOp {
     typedef SiluSrc<T> Src;
     static constexpr bool kNorm = false, kSilu = true;
+    Raw<T> x, r;
     static __device__ __forceinline__ Src src(const RowArgs& a, int64_t row) {
         return Src{static_cast<const T*>(a.x) + row * a.ldx, static_cast<const T*>(a.r) + row * a.ldr};
     }
-    static __device__ __forceinline__ void first(const RowArgs& a, int64_t row, int64_t k, int n, float (&p)[kChunk],
-                                                 uint32_t& top_ab) {
+    __device__ __forceinline__ void load(const RowArgs& a, int64_t row, int64_t k, int n) {
+        x.load(static_cast<const T*>(a.x) + row * a.ldx + k, n);
+        r.load(static_cast<const T*>(a.r) + row * a.ldr + k, n);
+    }
+    __device__ __forceinline__ void values(const RowArgs&, int64_t, int64_t, int, float (&p)[kChunk], uint32_t& top_ab) {
         float b[kChunk];
-        load_chunk(static_cast<const T*>(a.x) + row * a.ldx + k, n, p);
-        load_chunk(static_cast<const T*>(a.r) + row * a.ldr + k, n, b);
+        x.get(p);
+        r.get(b);
 #pragma unroll
         for (int j = 0; j < kChunk; ++j) {
             float ab;
@@ -342,11 +360,11 @@ struct SiluOp {
     }
     // Dense rows have no maximum to hide behind: gates below -80 and products
     // that overflow before the sigmoid are taken in fp64.
-    static __device__ __forceinline__ void dense(const RowArgs& a, int64_t row, int64_t k, int n, float (&p)[kChunk]) {
+    __device__ __forceinline__ void dense(const RowArgs& a, int64_t row, int64_t k, int n, float (&p)[kChunk]) {
         float b[kChunk];
         uint32_t mask = 0;
-        load_chunk(static_cast<const T*>(a.x) + row * a.ldx + k, n, p);
-        load_chunk(static_cast<const T*>(a.r) + row * a.ldr + k, n, b);
+        x.get(p);
+        r.get(b);
 #pragma unroll
         for (int j = 0; j < kChunk; ++j) {
             float ab;
@@ -354,7 +372,7 @@ struct SiluOp {
             p[j] = silu_mul_fast(p[j], b[j], ab);
             mask |= low || __builtin_fabsf(ab) > FLT_MAX ? 1u << j : 0u;
         }
-        mask &= n >= kChunk ? 0xffu : (1u << n) - 1u;
+        mask &= n >= kChunk ? 0xffu : (1u << max(n, 0)) - 1u;
         const Src s = src(a, row);
         while (mask) {
             const int h = __builtin_ctz(mask);
@@ -389,7 +407,11 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void row_kernel(RowArgs a) {
     float w[kNorm && NV > 0 ? NV : 1][kChunk];
     if constexpr (kNorm && NV > 0) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) load_chunk(a.weight + chunk_k(i), chunk_n(chunk_k(i)), w[i]);
+        for (int i = 0; i < NV; ++i) {
+            Raw<float> g;
+            g.load(a.weight + chunk_k(i), chunk_n(chunk_k(i)));
+            g.get(w[i]);
+        }
     }
 
     int parity = 0;
@@ -400,23 +422,28 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void row_kernel(RowArgs a) {
         uint32_t top = 0, top_ab = 0;
         double ss = 0.0;
 
-        auto take = [&](int i, float (&x)[kChunk]) {
+        auto values = [&](Op& op, int i, float (&x)[kChunk]) {
             const int64_t k = chunk_k(i);
-            const int n = chunk_n(k);
-            if (n > 0) {
-                if constexpr (Op::kSilu && kDense) Op::dense(a, row, k, n, x);
-                else Op::first(a, row, k, n, x, top_ab);
-            } else {
-#pragma unroll
-                for (int j = 0; j < kChunk; ++j) x[j] = 0.0f;
-            }
+            if constexpr (Op::kSilu && kDense) op.dense(a, row, k, chunk_n(k), x);
+            else op.values(a, row, k, chunk_n(k), x, top_ab);
         };
-        // The same values once more, of a row that first() has been through.
+        auto take = [&](int i, float (&x)[kChunk]) {
+            Op op;
+            op.load(a, row, chunk_k(i), chunk_n(chunk_k(i)));
+            values(op, i, x);
+        };
+        auto weight = [&](int i) {
+            Raw<float> g;
+            g.load(a.weight + chunk_k(i), chunk_n(chunk_k(i)));
+            g.get(w[0]);
+        };
+        // The same values once more, of a row that values() has been through.
         auto again = [&](int i, float (&x)[kChunk]) {
             if constexpr (kNorm) {
-                const int64_t k = chunk_k(i);
-                load_chunk(src.h + k, chunk_n(k), x);
-                load_chunk(src.w + k, chunk_n(k), w[0]);
+                Raw<std::remove_const_t<std::remove_pointer_t<decltype(src.h)>>> h;
+                h.load(src.h + chunk_k(i), chunk_n(chunk_k(i)));
+                h.get(x);
+                weight(i);
             } else {
                 take(i, x);
             }
@@ -432,8 +459,11 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void row_kernel(RowArgs a) {
             }
         };
         if constexpr (NV > 0) {
+            Op op[NV];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) take(i, v[i]);
+            for (int i = 0; i < NV; ++i) op[i].load(a, row, chunk_k(i), chunk_n(chunk_k(i)));
+#pragma unroll
+            for (int i = 0; i < NV; ++i) values(op[i], i, v[i]);
             if constexpr (kReduced) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) look(v[i], w[kNorm ? i : 0]);
@@ -441,7 +471,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void row_kernel(RowArgs a) {
         } else if constexpr (kReduced) {
             for (int i = 0; i < per; ++i) {
                 take(i, v[0]);
-                if constexpr (kNorm) load_chunk(src.w + chunk_k(i), chunk_n(chunk_k(i)), w[0]);
+                if constexpr (kNorm) weight(i);
                 look(v[0], w[0]);
             }
         }
