@@ -54,12 +54,23 @@ __device__ __forceinline__ float to_f(__bf16 v) { return static_cast<float>(v); 
 template <class T>
 struct Raw {
     T t[kChunk];
-    __device__ __forceinline__ void load(const T* p, int n) {
-        if (n >= kChunk) {
-            __builtin_memcpy(t, p, sizeof(t));
+    // The chunk at k of the row p. WHOLE: a thread without a chunk (k beyond
+    // the row, n = 0) reads the row's first and drops it: a test around the
+    // load would be a branch with a wait in it.
+    template <bool WHOLE>
+    __device__ __forceinline__ void load(const T* p, int64_t k, int n) {
+        if constexpr (WHOLE) {
+            constexpr int kWords = sizeof(t) / 4;
+            uint32_t u[kWords];
+            __builtin_memcpy(u, p + (n > 0 ? k : 0), sizeof(t));
+#pragma unroll
+            for (int j = 0; j < kWords; ++j) u[j] = n > 0 ? u[j] : 0u;
+            __builtin_memcpy(t, u, sizeof(t));
+        } else if (n >= kChunk) {
+            __builtin_memcpy(t, p + k, sizeof(t));
         } else {
 #pragma unroll
-            for (int j = 0; j < kChunk; ++j) t[j] = j < n ? p[j] : static_cast<T>(0.0f);
+            for (int j = 0; j < kChunk; ++j) t[j] = j < n ? p[k + j] : static_cast<T>(0.0f);
         }
     }
     __device__ __forceinline__ void get(float (&v)[kChunk]) const {
@@ -68,14 +79,14 @@ struct Raw {
     }
 };
 
-template <class T>
+template <bool WHOLE, class T>
 __device__ __forceinline__ void store_chunk(T* p, int n, const float (&v)[kChunk]) {
     if (n >= kChunk) {
         T t[kChunk];
 #pragma unroll
         for (int j = 0; j < kChunk; ++j) t[j] = static_cast<T>(v[j]);
         __builtin_memcpy(p, t, sizeof(t));
-    } else {
+    } else if constexpr (!WHOLE) {
 #pragma unroll
         for (int j = 0; j < kChunk; ++j)
             if (j < n) p[j] = static_cast<T>(v[j]);
@@ -212,10 +223,11 @@ __device__ __forceinline__ uint32_t bytes_set(u32x2 d) {
     return mask;
 }
 
+template <bool WHOLE>
 __device__ __forceinline__ void store_codes(uint8_t* p, int n, u32x2 w) {
     if (n >= kChunk) {
         __builtin_memcpy(p, &w, 8);
-    } else {
+    } else if constexpr (!WHOLE) {
 #pragma unroll
         for (int j = 0; j < kChunk; ++j)
             if (j < n) p[j] = static_cast<uint8_t>(w[j / 4] >> (8 * (j % 4)));
@@ -300,9 +312,11 @@ struct PlainOp {
     static __device__ __forceinline__ Src src(const RowArgs& a, int64_t row) {
         return Src{static_cast<const T*>(a.x) + row * a.ldx};
     }
+    template <bool WHOLE>
     __device__ __forceinline__ void load(const RowArgs& a, int64_t row, int64_t k, int n) {
-        x.load(static_cast<const T*>(a.x) + row * a.ldx + k, n);
+        x.template load<WHOLE>(static_cast<const T*>(a.x) + row * a.ldx, k, n);
     }
+    template <bool WHOLE>
     __device__ __forceinline__ void values(const RowArgs&, int64_t, int64_t, int, float (&p)[kChunk], uint32_t&) {
         x.get(p);
     }
@@ -317,12 +331,14 @@ struct NormOp {
         return a.r ? Src{static_cast<const T*>(a.sum) + row * a.lds, a.weight}
                    : Src{static_cast<const T*>(a.x) + row * a.ldx, a.weight};
     }
+    template <bool WHOLE>
     __device__ __forceinline__ void load(const RowArgs& a, int64_t row, int64_t k, int n) {
-        x.load(static_cast<const T*>(a.x) + row * a.ldx + k, n);
-        if (a.r) r.load(static_cast<const T*>(a.r) + row * a.ldr + k, n);
+        x.template load<WHOLE>(static_cast<const T*>(a.x) + row * a.ldx, k, n);
+        if (a.r) r.template load<WHOLE>(static_cast<const T*>(a.r) + row * a.ldr, k, n);
     }
     // h = x + residual in fp32, rounded once to the stream's type: what is
     // stored is what is normalised.
+    template <bool WHOLE>
     __device__ __forceinline__ void values(const RowArgs& a, int64_t row, int64_t k, int n, float (&h)[kChunk], uint32_t&) {
         x.get(h);
         if (a.r) {
@@ -330,7 +346,7 @@ struct NormOp {
             r.get(b);
 #pragma unroll
             for (int j = 0; j < kChunk; ++j) h[j] = to_f(static_cast<T>(h[j] + b[j]));
-            store_chunk(static_cast<T*>(a.sum) + row * a.lds + k, n, h);
+            store_chunk<WHOLE>(static_cast<T*>(a.sum) + row * a.lds + k, n, h);
         }
     }
 };
@@ -343,10 +359,12 @@ struct SiluOp {
     static __device__ __forceinline__ Src src(const RowArgs& a, int64_t row) {
         return Src{static_cast<const T*>(a.x) + row * a.ldx, static_cast<const T*>(a.r) + row * a.ldr};
     }
+    template <bool WHOLE>
     __device__ __forceinline__ void load(const RowArgs& a, int64_t row, int64_t k, int n) {
-        x.load(static_cast<const T*>(a.x) + row * a.ldx + k, n);
-        r.load(static_cast<const T*>(a.r) + row * a.ldr + k, n);
+        x.template load<WHOLE>(static_cast<const T*>(a.x) + row * a.ldx, k, n);
+        r.template load<WHOLE>(static_cast<const T*>(a.r) + row * a.ldr, k, n);
     }
+    template <bool WHOLE>
     __device__ __forceinline__ void values(const RowArgs&, int64_t, int64_t, int, float (&p)[kChunk], uint32_t& top_ab) {
         float b[kChunk];
         x.get(p);
@@ -388,7 +406,11 @@ struct SiluOp {
 // chunks of eight elements per thread held in registers: one pass over the
 // data. NV = 0: rows of any length, read again for each step. Workgroups take
 // rows in turn; the norm's weight stays in registers across them.
-template <class Op, int OUT, class OutT, int TPR, int NV>
+//
+// WHOLE: K is a multiple of eight, so no chunk is partial. Without it every
+// element of a chunk has a test of its own, which costs more than the work
+// (16384 x 8192 bf16: 17 vector instructions an element instead of 8).
+template <class Op, int OUT, class OutT, int TPR, int NV, bool WHOLE>
 __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void row_kernel(RowArgs a) {
     constexpr int RPB = TPR == 64 ? 4 : 1;
     constexpr bool kNorm = Op::kNorm, kDense = OUT == kOutDense;
@@ -402,14 +424,17 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void row_kernel(RowArgs a) {
     const int wave = threadIdx.x >> 6;
     const int per = NV > 0 ? NV : static_cast<int>((a.K + kChunk * TPR - 1) / (kChunk * TPR));
     auto chunk_k = [&](int i) { return static_cast<int64_t>(i * TPR + lane) * kChunk; };
-    auto chunk_n = [&](int64_t k) { return static_cast<int>(a.K - k < kChunk ? a.K - k : kChunk); };   // <= 0: none
+    auto chunk_n = [&](int64_t k) {                                                       // <= 0: none
+        if constexpr (WHOLE) return k < a.K ? kChunk : 0;
+        else return static_cast<int>(a.K - k < kChunk ? a.K - k : kChunk);
+    };
 
     float w[kNorm && NV > 0 ? NV : 1][kChunk];
     if constexpr (kNorm && NV > 0) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             Raw<float> g;
-            g.load(a.weight + chunk_k(i), chunk_n(chunk_k(i)));
+            g.load<WHOLE>(a.weight, chunk_k(i), chunk_n(chunk_k(i)));
             g.get(w[i]);
         }
     }
@@ -425,23 +450,23 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void row_kernel(RowArgs a) {
         auto values = [&](Op& op, int i, float (&x)[kChunk]) {
             const int64_t k = chunk_k(i);
             if constexpr (Op::kSilu && kDense) op.dense(a, row, k, chunk_n(k), x);
-            else op.values(a, row, k, chunk_n(k), x, top_ab);
+            else op.template values<WHOLE>(a, row, k, chunk_n(k), x, top_ab);
         };
         auto take = [&](int i, float (&x)[kChunk]) {
             Op op;
-            op.load(a, row, chunk_k(i), chunk_n(chunk_k(i)));
+            op.template load<WHOLE>(a, row, chunk_k(i), chunk_n(chunk_k(i)));
             values(op, i, x);
         };
         auto weight = [&](int i) {
             Raw<float> g;
-            g.load(a.weight + chunk_k(i), chunk_n(chunk_k(i)));
+            g.load<WHOLE>(a.weight, chunk_k(i), chunk_n(chunk_k(i)));
             g.get(w[0]);
         };
         // The same values once more, of a row that values() has been through.
         auto again = [&](int i, float (&x)[kChunk]) {
             if constexpr (kNorm) {
                 Raw<std::remove_const_t<std::remove_pointer_t<decltype(src.h)>>> h;
-                h.load(src.h + chunk_k(i), chunk_n(chunk_k(i)));
+                h.template load<WHOLE>(src.h, chunk_k(i), chunk_n(chunk_k(i)));
                 h.get(x);
                 weight(i);
             } else {
@@ -461,7 +486,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void row_kernel(RowArgs a) {
         if constexpr (NV > 0) {
             Op op[NV];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) op[i].load(a, row, chunk_k(i), chunk_n(chunk_k(i)));
+            for (int i = 0; i < NV; ++i) op[i].template load<WHOLE>(a, row, chunk_k(i), chunk_n(chunk_k(i)));
 #pragma unroll
             for (int i = 0; i < NV; ++i) values(op[i], i, v[i]);
             if constexpr (kReduced) {
@@ -510,7 +535,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void row_kernel(RowArgs a) {
 #pragma unroll
                     for (int j = 0; j < kChunk; ++j) x[j] = x[j] * rf * wx[j];
                 }
-                store_chunk(out + k, n, x);
+                store_chunk<WHOLE>(out + k, n, x);
             };
             if constexpr (NV > 0) {
 #pragma unroll
@@ -598,7 +623,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void row_kernel(RowArgs a) {
                     c = fast_codes<OUT>(p, lo, hi, d);
                     mask = d[0] | d[1] ? bytes_set(d) : 0u;
                 }
-                store_codes(out + k, n, c);
+                store_codes<WHOLE>(out + k, n, c);
                 return n >= kChunk ? mask : mask & ((1u << n) - 1u);
             };
             // The same thread stored these elements' chunk, so the bytes land in this order.
@@ -627,18 +652,24 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void row_kernel(RowArgs a) {
 
 constexpr int64_t kMaxGrid = 1 << 20;
 
-template <class Op, int OUT, class OutT, int TPR, int NV>
+template <class Op, int OUT, class OutT, int TPR, int NV, bool WHOLE = true>
 hipError_t launch_rows(const RowArgs& a, hipStream_t stream) {
     constexpr int RPB = TPR == 64 ? 4 : 1;
     const int64_t blocks = (a.M + RPB - 1) / RPB;
-    row_kernel<Op, OUT, OutT, TPR, NV><<<static_cast<uint32_t>(blocks < kMaxGrid ? blocks : kMaxGrid),
-                                         TPR == 64 ? 256 : TPR, 0, stream>>>(a);
+    row_kernel<Op, OUT, OutT, TPR, NV, WHOLE><<<static_cast<uint32_t>(blocks < kMaxGrid ? blocks : kMaxGrid),
+                                                TPR == 64 ? 256 : TPR, 0, stream>>>(a);
     return hipGetLastError();
 }
 
 // Threads and chunks per row by its length alone.
 template <class Op, int OUT, class OutT>
 hipError_t launch_by_length(const RowArgs& a, hipStream_t stream) {
+    if (a.K % kChunk != 0) {
+        if (a.K <= 64 * 8) return launch_rows<Op, OUT, OutT, 64, 1, false>(a, stream);
+        if (a.K <= 256 * 8) return launch_rows<Op, OUT, OutT, 256, 1, false>(a, stream);
+        if (a.K <= 256 * 32) return launch_rows<Op, OUT, OutT, 256, 4, false>(a, stream);
+        return launch_rows<Op, OUT, OutT, 1024, 0, false>(a, stream);
+    }
     if (a.K <= 64 * 8) return launch_rows<Op, OUT, OutT, 64, 1>(a, stream);
     if (a.K <= 64 * 16) return launch_rows<Op, OUT, OutT, 64, 2>(a, stream);
     if (a.K <= 256 * 8) return launch_rows<Op, OUT, OutT, 256, 1>(a, stream);
