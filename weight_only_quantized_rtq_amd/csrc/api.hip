@@ -606,7 +606,7 @@ rtq_status rtq_project_a8(const rtq_proj_a8* projs, int32_t n, int64_t M, void* 
         outs[i].width = static_cast<uintptr_t>(d.N) * size;
         tasks[i] = rtq::A8Task{static_cast<const uint8_t*>(d.x), d.x_scale, static_cast<const uint8_t*>(d.payload),
                                d.fmt == RTQ_FMT_Q8 ? d.scale : nullptr, d.bias, d.y, d.ldy, d.N, d.K, d.y_dtype,
-                               d.fmt == RTQ_FMT_Q8 ? rtq::kA8Int : d.y_dtype == RTQ_F32 ? rtq::kA8F8Wide : rtq::kA8F8};
+                               (d.fmt == RTQ_FMT_Q8 ? rtq::kA8Int : rtq::kA8F8) + (d.y_dtype == RTQ_F32 ? 1 : 0)};
     }
     if (M == 0) return RTQ_OK;
     // Outputs sorted by their first byte; top = the furthest end so far, so an

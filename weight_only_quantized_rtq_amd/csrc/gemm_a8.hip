@@ -27,14 +27,14 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kBK = 128;                   // bytes (= elements) of K per stage
+constexpr int kBand = 4;                   // tiles of m that a band of tiles covers
+
+constexpr bool is_int(int kind) { return kind == kA8Int || kind == kA8IntWide; }
+constexpr bool is_wide(int kind) { return kind == kA8IntWide || kind == kA8F8Wide; }
 
 template <int KIND>
 struct Acc {
-    typedef floatx4 T;
-};
-template <>
-struct Acc<kA8Int> {
-    typedef i32x4 T;
+    typedef std::conditional_t<is_int(KIND), i32x4, floatx4> T;
 };
 
 // Eight E4M3 codes -> bf16, exactly.
@@ -51,7 +51,7 @@ __device__ __forceinline__ bf16x8 f8_to_bf16(int w0, int w1) {
 // operand (the same k of both, so their order within the lane is free).
 template <int KIND>
 __device__ __forceinline__ typename Acc<KIND>::T mma(i32x4 a0, i32x4 a1, i32x4 b0, i32x4 b1, typename Acc<KIND>::T c) {
-    if constexpr (KIND == kA8Int) {
+    if constexpr (is_int(KIND)) {
         c = __builtin_amdgcn_mfma_i32_16x16x64_i8(a0, b0, c, 0, 0, 0);
         return __builtin_amdgcn_mfma_i32_16x16x64_i8(a1, b1, c, 0, 0, 0);
     } else if constexpr (KIND == kA8F8) {
@@ -106,27 +106,34 @@ __device__ __forceinline__ floatx4 channels(const float* p, int n, int N, float 
     return v;
 }
 
-// y[n .. n+3] of one row: sum * (row scale * channel scale) + bias in fp32, rounded once.
-template <class T, class V>
-__device__ __forceinline__ void put4(T* y, int n, int N, V acc, float s, floatx4 sw, floatx4 bias) {
-    T w[4];
+// y[n .. n+C-1] of one row, in one store of up to 16 bytes: sum * (row scale *
+// channel scale) + bias in fp32, rounded once. Nontemporal: y is not read
+// here, and lines held back to be completed in L2 evict what is (65536 x 2048
+// x 512 int8 to fp32: 201 us without, 168 with).
+template <int C, class T>
+__device__ __forceinline__ void put(T* y, int n, int N, const float (&v)[C]) {
+    typedef T V __attribute__((ext_vector_type(C), aligned(sizeof(T))));
+    V w;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = static_cast<T>(static_cast<float>(acc[e]) * (s * sw[e]) + bias[e]);
-    if (n + 4 <= N) {
-        __builtin_memcpy(y + n, w, sizeof(w));
+    for (int e = 0; e < C; ++e) w[e] = static_cast<T>(v[e]);
+    if (n + C <= N) {
+        __builtin_nontemporal_store(w, reinterpret_cast<V*>(y + n));
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < C; ++e)
             if (n + e < N) y[n + e] = w[e];
     }
 }
 
 // f(pointer of y's type)
-template <class F>
+template <int KIND, class F>
 __device__ __forceinline__ void by_type(const A8Task& t, F f) {
-    if (t.y_dtype == RTQ_F32) f(static_cast<float*>(t.y));
-    else if (t.y_dtype == RTQ_F16) f(static_cast<_Float16*>(t.y));
-    else f(static_cast<__bf16*>(t.y));
+    if constexpr (is_wide(KIND)) {
+        f(static_cast<float*>(t.y));
+    } else {
+        if (t.y_dtype == RTQ_F16) f(static_cast<_Float16*>(t.y));
+        else f(static_cast<__bf16*>(t.y));
+    }
 }
 
 // ---- few rows: weights straight to registers, K split over the waves ----
@@ -188,16 +195,37 @@ __global__ __launch_bounds__(W * 64) void skinny_kernel(const A8Args args) {
         const int n = n0 + g * 4;
         if (m < args.M && n < t.N) {
             const floatx4 sw = channels(t.w_scale, n, t.N, 1.0f), bias = channels(t.bias, n, t.N, 0.0f);
-            by_type(t, [&](auto* y) { put4(y + m * t.ldy, n, t.N, sum, t.x_scale[m], sw, bias); });
+            const float s = t.x_scale[m];
+            float y4[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y4[e] = static_cast<float>(sum[e]) * (s * sw[e]) + bias[e];
+            by_type<KIND>(t, [&](auto* y) { put(y + m * t.ldy, n, t.N, y4); });
         }
     }
 }
 
 // ---- tiles through LDS ----
 
-// LDS: rows of 128 bytes, the 16-byte chunk c of row r at slot c ^ (r & 7):
-// the 16 rows of an operand read hit every bank group evenly.
-__device__ __forceinline__ int lds_at(int r, int c) { return r * kBK + ((c ^ (r & 7)) << 4); }
+// Which n of a wave's tile is row a (0 .. 15) of its block i. A lane ends with
+// rows 4g .. 4g+3 of every block (g = lane / 16); with a 16-bit y the rows of
+// two blocks interleave in fours, so a lane's eight n of a pair are adjacent
+// and leave in one 16-byte store.
+template <bool WIDE>
+__device__ __forceinline__ int n_row(int i, int a) {
+    if constexpr (WIDE) return i * 16 + a;
+    else return (i >> 1) * 32 + (a >> 2) * 8 + (i & 1) * 4 + (a & 3);
+}
+
+// LDS: rows of 128 bytes, the 16-byte chunk c of row r at slot c ^ key(r): the
+// eight rows that are read together have eight keys, so they cover all banks.
+// key is r & 7 where those are rows 0 .. 7 or 8 .. 15, and for the interleaved
+// n rows, 0 .. 3 with 8 .. 11, bit 3 of r takes the place of bit 2.
+template <bool PLAIN>
+__device__ __forceinline__ int lds_key(int r) {
+    return PLAIN ? r & 7 : (r & 3) | ((r >> 1) & 4);
+}
+template <bool PLAIN>
+__device__ __forceinline__ int lds_at(int r, int c) { return r * kBK + ((c ^ lds_key<PLAIN>(r)) << 4); }
 
 __device__ const uint32_t zero_chunk[4] = {0, 0, 0, 0};
 
@@ -221,13 +249,18 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(const A8Args args) {
     constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
     constexpr int OPS = ROWS / 8 / NW;                         // 1 KB copies of 8 rows, per wave and stage
     static_assert(ROWS % (8 * NW) == 0 && BM % (8 * NW) == 0, "copies divide over the waves");
+    static_assert(NW % 2 == 0 && BM % 16 == 0 && TN % 2 == 0, "keys and pairs of blocks");
     __shared__ __align__(1024) uint8_t lds[2][ROWS * kBK];     // rows 0 .. BM-1: x, then the weights
     int tile;
-    const A8Task& t = task_of(args, blockIdx.x, tile);
+    const A8Task& t = task_of(args, xcd_remap_split(blockIdx.x, args.total), tile);
     const int K = t.K;
-    const int tiles_n = (t.N + BN - 1) / BN;
-    const int64_t m0 = static_cast<int64_t>(tile / tiles_n) * BM;
-    const int n0 = tile % tiles_n * BN;
+    // Each XCD works on a run of tiles; a run goes through bands of kBand
+    // tiles of m, so the tiles in flight on it share rows and weights in its L2.
+    const int tiles_n = (t.N + BN - 1) / BN, tiles_m = static_cast<int>((args.M + BM - 1) / BM);
+    const int band = tile / (kBand * tiles_n), in_band = tile % (kBand * tiles_n);
+    const int high = min(kBand, tiles_m - band * kBand);
+    const int64_t m0 = static_cast<int64_t>(band * kBand + in_band % high) * BM;
+    const int n0 = in_band / high * BN;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wm = wave % WM * (TM * 16), wn = wave / WM * (TN * 16);
     const int r16 = lane & 15, g = lane >> 4;
@@ -235,7 +268,11 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(const A8Args args) {
     const uint8_t* wb = t.w + static_cast<int64_t>(n0) * K;
 
     // Copy j of this wave: rows 8 (j NW + wave) .. + 7, lane: row lane / 8, slot lane % 8.
-    const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;         // (8 j + lane / 8) & 7 = lane / 8
+    // The key of such a row depends on lane / 8 and, for the weights' interleave,
+    // on the parity of wave (NW and BM / 8 are even).
+    constexpr bool kWide = is_wide(KIND);
+    const int chunk_x = ((lane & 7) ^ lds_key<true>(lane >> 3)) * 16;
+    const int chunk_w = ((lane & 7) ^ lds_key<kWide>((lane >> 3) + 8 * (wave & 1))) * 16;
     uint32_t off[OPS];
 #pragma unroll
     for (int j = 0; j < OPS; ++j) {
@@ -250,6 +287,7 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(const A8Args args) {
 #pragma unroll
         for (int j = 0; j < OPS; ++j) {
             const uint8_t* base = j * NW * 8 < BM ? xb : wb;
+            const int chunk = j * NW * 8 < BM ? chunk_x : chunk_w;
             if constexpr (ALIGNED) {
                 const uint8_t* src = base + k0 + (off[j] + chunk);
                 if (k0 + kBK > K && k0 + chunk >= K) src = reinterpret_cast<const uint8_t*>(zero_chunk);
@@ -289,45 +327,52 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(const A8Args args) {
 #pragma unroll
         for (int q = 0; q < TM; ++q)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) b[q][h] = *reinterpret_cast<const i32x4*>(xs + lds_at(q * 16 + r16, g + 4 * h));
+            for (int h = 0; h < 2; ++h) b[q][h] = *reinterpret_cast<const i32x4*>(xs + lds_at<true>(q * 16 + r16, g + 4 * h));
 #pragma unroll
         for (int i = 0; i < TN; ++i) {
             i32x4 a[2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) a[h] = *reinterpret_cast<const i32x4*>(ws + lds_at(i * 16 + r16, g + 4 * h));
+            for (int h = 0; h < 2; ++h) a[h] = *reinterpret_cast<const i32x4*>(ws + lds_at<kWide>(n_row<kWide>(i, r16), g + 4 * h));
 #pragma unroll
             for (int q = 0; q < TM; ++q) acc[i][q] = mma<KIND>(a[0], a[1], b[q][0], b[q][1], acc[i][q]);
         }
         if (more) settle(buf ^ 1);
     }
 
-    // Lane: column m = lane % 16, rows n = 4 (lane / 16) .. + 3 of each block.
-    const int mq = wm + r16, nq = n0 + wn + g * 4;
+    // Lane: m = lane % 16 of each block q; C adjacent n of each group of
+    // blocks, as n_row puts them.
+    constexpr int C = kWide ? 4 : 8, P = C / 4;                // n of a store, blocks it takes
+    const int mq = wm + r16, nq = n0 + wn + g * C;
     const int M = args.M - m0 < BM ? static_cast<int>(args.M - m0) : BM;     // rows of this tile
     float sx[TM];
 #pragma unroll
     for (int q = 0; q < TM; ++q) sx[q] = t.x_scale[m0 + min(mq + q * 16, M - 1)];
-    by_type(t, [&](auto* y) {
+    by_type<KIND>(t, [&](auto* y) {
         y += m0 * t.ldy;
-        if (M == BM && n0 + BN <= t.N) {
+        auto finish = [&](int rows, int N) {
 #pragma unroll
-            for (int i = 0; i < TN; ++i) {
+            for (int i = 0; i < TN; i += P) {
                 const int n = nq + i * 16;
-                const floatx4 sw = channels(t.w_scale, n, 1 << 30, 1.0f), bias = channels(t.bias, n, 1 << 30, 0.0f);
+                if (n >= N) continue;
+                floatx4 sw[P], bias[P];
 #pragma unroll
-                for (int q = 0; q < TM; ++q) put4(y + (mq + q * 16) * t.ldy, n, 1 << 30, acc[i][q], sx[q], sw, bias);
+                for (int p = 0; p < P; ++p) {
+                    sw[p] = channels(t.w_scale, n + 4 * p, N, 1.0f);
+                    bias[p] = channels(t.bias, n + 4 * p, N, 0.0f);
+                }
+#pragma unroll
+                for (int q = 0; q < TM; ++q) {
+                    if (mq + q * 16 >= rows) continue;
+                    float v[C];
+#pragma unroll
+                    for (int e = 0; e < C; ++e)
+                        v[e] = static_cast<float>(acc[i + e / 4][q][e % 4]) * (sx[q] * sw[e / 4][e % 4]) + bias[e / 4][e % 4];
+                    put(y + (mq + q * 16) * t.ldy, n, N, v);
+                }
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < TN; ++i) {
-                const int n = nq + i * 16;
-                if (n >= t.N) continue;
-                const floatx4 sw = channels(t.w_scale, n, t.N, 1.0f), bias = channels(t.bias, n, t.N, 0.0f);
-#pragma unroll
-                for (int q = 0; q < TM; ++q)
-                    if (mq + q * 16 < M) put4(y + (mq + q * 16) * t.ldy, n, t.N, acc[i][q], sx[q], sw, bias);
-            }
-        }
+        };
+        if (M == BM && n0 + BN <= t.N) finish(1 << 30, 1 << 30);       // a whole tile: no tests
+        else finish(M, t.N);
     });
 }
 
@@ -338,6 +383,7 @@ uint32_t number(A8Args& args, int BM, int BN) {
         args.begin[j] = static_cast<uint32_t>(tiles);
         tiles += ((args.M + BM - 1) / BM) * ((args.task[j].N + BN - 1) / BN);
     }
+    args.total = static_cast<int32_t>(tiles);
     return static_cast<uint32_t>(tiles);
 }
 
@@ -401,10 +447,14 @@ hipError_t launch_a8(const A8Task* tasks, int count, int64_t M, hipStream_t stre
                     t.x_scale += m;
                     t.y = static_cast<uint8_t*>(t.y) + m * t.ldy * (t.y_dtype == RTQ_F32 ? 4 : 2);
                 }
-                const hipError_t e =
-                    kind == kA8Int  ? (whole ? launch_kind<kA8Int, true>(args, stream) : launch_kind<kA8Int, false>(args, stream))
-                    : kind == kA8F8 ? (whole ? launch_kind<kA8F8, true>(args, stream) : launch_kind<kA8F8, false>(args, stream))
-                                    : (whole ? launch_kind<kA8F8Wide, true>(args, stream) : launch_kind<kA8F8Wide, false>(args, stream));
+                auto run = [&](auto k) {
+                    constexpr int KIND = decltype(k)::value;
+                    return whole ? launch_kind<KIND, true>(args, stream) : launch_kind<KIND, false>(args, stream);
+                };
+                const hipError_t e = kind == kA8Int       ? run(std::integral_constant<int, kA8Int>())
+                                     : kind == kA8IntWide ? run(std::integral_constant<int, kA8IntWide>())
+                                     : kind == kA8F8      ? run(std::integral_constant<int, kA8F8>())
+                                                          : run(std::integral_constant<int, kA8F8Wide>());
                 if (e != hipSuccess) return e;
             }
         }

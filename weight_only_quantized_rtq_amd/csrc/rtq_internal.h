@@ -108,9 +108,9 @@ hipError_t launch_rms_norm(const void* x, int64_t ldx, const void* residual, int
 hipError_t launch_silu_mul(const void* x, int64_t lda, const void* b, int64_t ldb, int dtype, int fmt, int out_dtype,
                            void* out, float* scale, int64_t M, int64_t K, hipStream_t stream);
 
-// 8-bit activations times 8-bit weights (gemm_a8.hip). Kinds of sums: int8;
-// E4M3 for 16-bit outputs; E4M3 in bf16 operands, for fp32 outputs.
-enum A8Kind : int { kA8Int = 0, kA8F8 = 1, kA8F8Wide = 2, kA8Kinds = 3 };
+// 8-bit activations times 8-bit weights (gemm_a8.hip). Kinds of products: int8
+// or E4M3, with a 16-bit y or (wide) an fp32 one.
+enum A8Kind : int { kA8Int = 0, kA8IntWide = 1, kA8F8 = 2, kA8F8Wide = 3, kA8Kinds = 4 };
 struct A8Task {
     const uint8_t* x;        // [M][K] codes
     const float* x_scale;    // [M]
@@ -130,6 +130,7 @@ struct A8Args {
     int64_t M;
     uint32_t begin[kA8Slots];    // first workgroup of each task
     int32_t count;
+    int32_t total;               // workgroups
 };
 // Tasks of any kinds, all sharing M.
 hipError_t launch_a8(const A8Task* tasks, int count, int64_t M, hipStream_t stream);
