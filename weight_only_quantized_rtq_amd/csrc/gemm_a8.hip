@@ -69,13 +69,32 @@ __device__ __forceinline__ typename Acc<KIND>::T mma(i32x4 a0, i32x4 a1, i32x4 b
     }
 }
 
-// 16 bytes of a row at k, zeros past K. ALIGNED: K a multiple of 16.
-template <bool ALIGNED>
+// 16 bytes v, the first `s` dropped (s >= 0; zeros come in behind).
+__device__ __forceinline__ i32x4 drop_bytes(i32x4 v, int s) {
+    const int zero = 0, q = s >> 2;
+    i32x4 a, b, c;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a[j] = q & 1 ? (j < 3 ? v[j + 1] : zero) : v[j];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b[j] = q & 2 ? (j < 2 ? a[j + 2] : zero) : a[j];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        c[j] = static_cast<int>(__builtin_amdgcn_alignbyte(static_cast<uint32_t>(j < 3 ? b[j + 1] : zero),
+                                                           static_cast<uint32_t>(b[j]), static_cast<uint32_t>(s & 3)));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[j] = s < 16 ? c[j] : zero;
+    return c;
+}
+
+// 16 bytes of a row of K at k, zeros past K. A chunk that the row ends in is
+// the row's last 16 bytes, shifted: one load without a branch.
 __device__ __forceinline__ i32x4 load16(const uint8_t* row, int k, int K) {
     i32x4 v = {0, 0, 0, 0};
-    if (k + 16 <= K) {
-        __builtin_memcpy(&v, row + k, 16);
-    } else if (!ALIGNED && k < K) {
+    if (K >= 16) {
+        const int at = min(k, K - 16);
+        __builtin_memcpy(&v, row + at, 16);
+        v = drop_bytes(v, k - at);
+    } else {
 #pragma unroll
         for (int j = 0; j < 15; ++j)
             if (k + j < K) v[j / 4] |= static_cast<int>(row[k + j]) << (8 * (j % 4));
@@ -106,8 +125,13 @@ __device__ __forceinline__ floatx4 channels(const float* p, int n, int N, float 
     return v;
 }
 
-// y[n .. n+C-1] of one row, in one store of up to 16 bytes: sum * (row scale *
-// channel scale) + bias in fp32, rounded once. Nontemporal: y is not read
+// An output in fp32: sum * (row scale * channel scale) + bias.
+template <class T>
+__device__ __forceinline__ float scaled(T sum, float s, float sw, float bias) {
+    return __builtin_fmaf(static_cast<float>(sum), s * sw, bias);
+}
+
+// y[n .. n+C-1] of one row, in one store of up to 16 bytes. Nontemporal: y is not read
 // here, and lines held back to be completed in L2 evict what is (65536 x 2048
 // x 512 int8 to fp32: 201 us without, 168 with).
 template <int C, class T>
@@ -115,7 +139,13 @@ __device__ __forceinline__ void put(T* y, int n, int N, const float (&v)[C]) {
     typedef T V __attribute__((ext_vector_type(C), aligned(sizeof(T))));
     V w;
 #pragma unroll
-    for (int e = 0; e < C; ++e) w[e] = static_cast<T>(v[e]);
+    for (int e = 0; e < C; ++e) {
+        float f = v[e];
+        // the fp32 value itself: fused with the conversion to fp16 the last
+        // operation would round once, in some kernels and not in others
+        if constexpr (__is_same(T, _Float16)) asm("" : "+v"(f));
+        w[e] = static_cast<T>(f);
+    }
     if (n + C <= N) {
         __builtin_nontemporal_store(w, reinterpret_cast<V*>(y + n));
     } else {
@@ -177,11 +207,18 @@ __global__ __launch_bounds__(W * 64) void skinny_kernel(const A8Args args) {
         }
     }
     if (k < K) {                                               // the last, partial step
-        const int left = K - g * 16;
-        const i32x4 a0 = load16<ALIGNED>(w, k, left), a1 = load16<ALIGNED>(w, k + 64, left);
+        auto last = [&](const uint8_t* p, int at) {            // p is 16 g into its row
+            if constexpr (ALIGNED) {
+                i32x4 v = {0, 0, 0, 0};
+                if (at + g * 16 < K) __builtin_memcpy(&v, p + at, 16);
+                return v;
+            } else {
+                return load16(p - g * 16, at + g * 16, K);
+            }
+        };
+        const i32x4 a0 = last(w, k), a1 = last(w, k + 64);
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-            acc[i] = mma<KIND>(a0, a1, load16<ALIGNED>(x[i], k, left), load16<ALIGNED>(x[i], k + 64, left), acc[i]);
+        for (int i = 0; i < MT; ++i) acc[i] = mma<KIND>(a0, a1, last(x[i], k), last(x[i], k + 64), acc[i]);
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
@@ -198,7 +235,7 @@ __global__ __launch_bounds__(W * 64) void skinny_kernel(const A8Args args) {
             const float s = t.x_scale[m];
             float y4[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y4[e] = static_cast<float>(sum[e]) * (s * sw[e]) + bias[e];
+            for (int e = 0; e < 4; ++e) y4[e] = scaled(sum[e], s, sw[e], bias[e]);
             by_type<KIND>(t, [&](auto* y) { put(y + m * t.ldy, n, t.N, y4); });
         }
     }
@@ -240,17 +277,18 @@ __device__ __forceinline__ void dma16(const uint8_t* src, uint8_t* lds_base) {
                                      (__attribute__((address_space(3))) void*)lds_base, 16, 0, 0);
 }
 
-// BM x BN outputs by WM x WN waves, stages of 128 of K in two LDS buffers: a
-// stage is copied (DMA to LDS, or through registers where rows are not
-// 16-byte aligned) while the one before it is multiplied.
-template <int KIND, int BM, int BN, int WM, int WN, bool ALIGNED>
+// BM x BN outputs by WM x WN waves, stages of 128 of K in S LDS buffers: the
+// next S - 1 stages are copied (DMA to LDS, or through registers, S = 2, where
+// rows are not 16-byte aligned) while one is multiplied.
+template <int KIND, int BM, int BN, int WM, int WN, int S, bool ALIGNED>
 __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(const A8Args args) {
     constexpr int NW = WM * WN, ROWS = BM + BN;
     constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
     constexpr int OPS = ROWS / 8 / NW;                         // 1 KB copies of 8 rows, per wave and stage
     static_assert(ROWS % (8 * NW) == 0 && BM % (8 * NW) == 0, "copies divide over the waves");
     static_assert(NW % 2 == 0 && BM % 16 == 0 && TN % 2 == 0, "keys and pairs of blocks");
-    __shared__ __align__(1024) uint8_t lds[2][ROWS * kBK];     // rows 0 .. BM-1: x, then the weights
+    static_assert(ALIGNED || S == 2, "copies through registers run one stage ahead");
+    __shared__ __align__(1024) uint8_t lds[S][ROWS * kBK];     // rows 0 .. BM-1: x, then the weights
     int tile;
     const A8Task& t = task_of(args, xcd_remap_split(blockIdx.x, args.total), tile);
     const int K = t.K;
@@ -293,7 +331,8 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(const A8Args args) {
                 if (k0 + kBK > K && k0 + chunk >= K) src = reinterpret_cast<const uint8_t*>(zero_chunk);
                 dma16(src, &lds[buf][(j * NW + wave) * 1024]);
             } else {
-                hold[j] = load16<false>(base + off[j], k0 + chunk, K);
+                if (k0 + kBK <= K) __builtin_memcpy(&hold[j], base + off[j] + k0 + chunk, 16);
+                else hold[j] = load16(base + off[j], k0 + chunk, K);
             }
         }
     };
@@ -306,21 +345,28 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(const A8Args args) {
     };
 
     typename Acc<KIND>::T acc[TN][TM] = {};
-    issue(0, 0);
+    const int steps = (K + kBK - 1) / kBK;
+#pragma unroll
+    for (int j = 0; j < S - 1; ++j)
+        if (j < steps) issue(j * kBK, j);
     settle(0);
-    for (int k0 = 0, buf = 0; k0 < K; k0 += kBK, buf ^= 1) {
+    for (int step = 0, buf = 0; step < steps; ++step, buf = buf + 1 < S ? buf + 1 : 0) {
         if constexpr (ALIGNED) {
             // Nothing moves past here: the last stage's LDS reads are all
             // used, so complete, before the barrier that frees their buffer.
             __builtin_amdgcn_sched_barrier(0);
-            wait_vm<0>();                                      // this wave's part of the stage
+            // This wave's part of the stage: the S - 2 stages issued after it
+            // may stay in flight (near the end there are fewer: wait for all).
+            if (S == 2 || step + S - 1 > steps) wait_vm<0>();
+            else wait_vm<(S - 2) * OPS>();
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
         } else {
             __syncthreads();
         }
-        const bool more = k0 + kBK < K;
-        if (more) issue(k0 + kBK, buf ^ 1);
+        const int ahead = buf > 0 ? buf - 1 : S - 1;           // (buf + S - 1) % S: the stage before this one's
+        const bool more = step + S - 1 < steps;
+        if (more) issue((step + S - 1) * kBK, ahead);
         const uint8_t* xs = lds[buf] + wm * kBK;
         const uint8_t* ws = lds[buf] + (BM + wn) * kBK;
         i32x4 b[TM][2];
@@ -328,15 +374,22 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(const A8Args args) {
         for (int q = 0; q < TM; ++q)
 #pragma unroll
             for (int h = 0; h < 2; ++h) b[q][h] = *reinterpret_cast<const i32x4*>(xs + lds_at<true>(q * 16 + r16, g + 4 * h));
+        // While one wave of a SIMD reads operands the other's matrix instructions
+        // go first (8192^3 E4M3: 414 -> 409 us; with the bf16 conversions between
+        // them it costs instead, 55.7 -> 66.7 us for 16384 x 2048 x 512).
+        if constexpr (KIND != kA8F8Wide) __builtin_amdgcn_s_setprio(1);
+        i32x4 a[TN][2];
 #pragma unroll
-        for (int i = 0; i < TN; ++i) {
-            i32x4 a[2];
+        for (int i = 0; i < TN; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) a[h] = *reinterpret_cast<const i32x4*>(ws + lds_at<kWide>(n_row<kWide>(i, r16), g + 4 * h));
+            for (int h = 0; h < 2; ++h)
+                a[i][h] = *reinterpret_cast<const i32x4*>(ws + lds_at<kWide>(n_row<kWide>(i, r16), g + 4 * h));
 #pragma unroll
-            for (int q = 0; q < TM; ++q) acc[i][q] = mma<KIND>(a[0], a[1], b[q][0], b[q][1], acc[i][q]);
-        }
-        if (more) settle(buf ^ 1);
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+            for (int q = 0; q < TM; ++q) acc[i][q] = mma<KIND>(a[i][0], a[i][1], b[q][0], b[q][1], acc[i][q]);
+        if constexpr (KIND != kA8F8Wide) __builtin_amdgcn_s_setprio(0);
+        if (more) settle(ahead);
     }
 
     // Lane: m = lane % 16 of each block q; C adjacent n of each group of
@@ -366,7 +419,7 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(const A8Args args) {
                     float v[C];
 #pragma unroll
                     for (int e = 0; e < C; ++e)
-                        v[e] = static_cast<float>(acc[i + e / 4][q][e % 4]) * (sx[q] * sw[e / 4][e % 4]) + bias[e / 4][e % 4];
+                        v[e] = scaled(acc[i + e / 4][q][e % 4], sx[q], sw[e / 4][e % 4], bias[e / 4][e % 4]);
                     put(y + (mq + q * 16) * t.ldy, n, N, v);
                 }
             }
@@ -387,6 +440,19 @@ uint32_t number(A8Args& args, int BM, int BN) {
     return static_cast<uint32_t>(tiles);
 }
 
+// Whether 256 x 256 tiles, one a CU, pay where there are enough of them. An
+// fp32 y of a short K is all stores, which two smaller tiles a CU overlap
+// better with loads (65536 x 2048 x 512: 153 us of 128 x 128, 165 us of 256 x
+// 256; 65536 x 512 x 2048: 125 and 91; a bf16 y of K = 512: 117 and 104).
+template <int KIND, bool ALIGNED>
+bool large_pays(const A8Args& args) {
+    if constexpr (!ALIGNED && KIND == kA8F8Wide) return false;     // its staging does not fit the registers
+    if (!is_wide(KIND)) return true;
+    for (int j = 0; j < args.count; ++j)
+        if (args.task[j].K < 1024) return false;
+    return true;
+}
+
 template <int KIND, bool ALIGNED>
 hipError_t launch_kind(A8Args& args, hipStream_t stream) {
     auto skinny = [&](auto mt, auto w) {
@@ -394,23 +460,46 @@ hipError_t launch_kind(A8Args& args, hipStream_t stream) {
         skinny_kernel<KIND, MT, W, ALIGNED><<<number(args, 16 * MT, 16), W * 64, 0, stream>>>(args);
         return hipGetLastError();
     };
-    auto tiles = [&](auto bm, auto bn, auto wm, auto wn) {
+    auto tiles = [&](auto bm, auto bn, auto wm, auto wn, auto stages) {
         constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value;
-        constexpr int WM = decltype(wm)::value, WN = decltype(wn)::value;
-        tile_kernel<KIND, BM, BN, WM, WN, ALIGNED><<<number(args, BM, BN), WM * WN * 64, 0, stream>>>(args);
+        constexpr int WM = decltype(wm)::value, WN = decltype(wn)::value, S = ALIGNED ? decltype(stages)::value : 2;
+        tile_kernel<KIND, BM, BN, WM, WN, S, ALIGNED><<<number(args, BM, BN), WM * WN * 64, 0, stream>>>(args);
         return hipGetLastError();
     };
-    using std::integral_constant;
-    if (args.M <= 16) return skinny(integral_constant<int, 1>(), integral_constant<int, 8>());
-    if (args.M <= 128) return skinny(integral_constant<int, 2>(), integral_constant<int, 4>());
-    if (number(args, 128, 128) < 512)
-        return tiles(integral_constant<int, 64>(), integral_constant<int, 64>(), integral_constant<int, 2>(),
-                     integral_constant<int, 2>());
-    if (number(args, 256, 256) < 512)
-        return tiles(integral_constant<int, 128>(), integral_constant<int, 128>(), integral_constant<int, 2>(),
-                     integral_constant<int, 2>());
-    return tiles(integral_constant<int, 256>(), integral_constant<int, 256>(), integral_constant<int, 4>(),
-                 integral_constant<int, 2>());
+    constexpr std::integral_constant<int, 1> c1{};
+    constexpr std::integral_constant<int, 2> c2{};
+    constexpr std::integral_constant<int, 4> c4{};
+    constexpr std::integral_constant<int, 8> c8{};
+    constexpr std::integral_constant<int, 32> c32{};
+    constexpr std::integral_constant<int, 64> c64{};
+    constexpr std::integral_constant<int, 128> c128{};
+    constexpr std::integral_constant<int, 256> c256{};
+    // Larger blocks read less, smaller ones keep 256 CUs busy: by the call's
+    // count of blocks of each size. us, int8 to bf16, M x N x K, as graph
+    // replays (the count in brackets):
+    //   16 x 16 straight to registers / 32 x 64 tiles: 80 x 512 x 512 (160) 3.3 / 4.1;
+    //     64 x 2048 x 8192 (512) 13.9 / 22.6; 128 x 2048 x 512 (1024) 4.4 / 4.1
+    //   one / two blocks of m a wave: 64 x 512 x 8192 (128) 10.0 / 13.5; 64 x 2048 x 8192 (512) 17.4 / 13.9
+    //   32 x 64 / 64 x 64: 512 x 2048 x 2048 (512) 9.2 / 9.4; 700 x 2048 x 8192 (704) 32.0 / 28.7
+    //   64 x 64 / 128 x 128: 1024 x 2048 x 8192 (512) 29.8 / 40.8; 1500 x 2048 x 8192 (768) 56.2 / 44.8
+    //   128 x 128 of eight waves and four stages, one a CU / of four waves and
+    //     two stages, two a CU: 2048 x 2048 x 8192 (256) 43.0 / 47.7; 3000 x 2048 x 8192 (384) 83.4 / 54.9
+    //   128 x 128 / 256 x 256: a round of 512 takes 0.57 of a round of 256 of
+    //     the large ones (63.6 us and 111.6 us at K = 8192)
+    // Rows through registers (two stages only): 16 x 16 / 32 x 64: 77 x 513 x
+    // 2053 (165) 8.3 / 12.5, 250 x 513 x 515 (528) 8.0 / 6.6; 32 x 64 / 64 x
+    // 64: 515 x 2051 x 2053 (561) 21.5 / 23.1, 1030 x 2051 x 2053 (1089) 29.7 / 27.6.
+    const int64_t n16 = number(args, 16, 16);
+    if (args.M <= 16) return skinny(c1, c8);
+    if (n16 <= (ALIGNED ? 600 : 300)) return n16 < 384 ? skinny(c1, c8) : skinny(c2, c8);
+    if (number(args, 32, 64) <= (ALIGNED ? 512 : 768)) return tiles(c32, c64, c2, c2, c4);
+    if (number(args, 64, 64) <= 512) return tiles(c64, c64, c2, c2, c4);
+    const int64_t n128 = number(args, 128, 128), n256 = number(args, 256, 256);
+    if (n128 <= 256) return tiles(c128, c128, c4, c2, c4);
+    const int64_t rounds128 = (n128 + 511) / 512 * 4, rounds256 = (n256 + 255) / 256 * 7;
+    if (rounds128 < rounds256 || !large_pays<KIND, ALIGNED>(args)) return tiles(c128, c128, c2, c2, c2);
+    if constexpr (ALIGNED || KIND != kA8F8Wide) return tiles(c256, c256, c4, c2, c2);
+    return tiles(c128, c128, c2, c2, c2);
 }
 
 bool task_aligned(const A8Task& t) {
