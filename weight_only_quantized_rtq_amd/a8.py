@@ -51,11 +51,13 @@ class A8Rows:
         return FMT_Q8 if self.codes.dtype == torch.int8 else FMT_F8
 
     def validate(self) -> None:
-        _need(self.codes, torch.int8 if self.codes.dtype == torch.int8 else torch.uint8, "codes")
-        _need(self.scale, torch.float32, "scale")
-        if self.codes.dim() != 2 or tuple(self.scale.shape) != (self.codes.shape[0],):
-            raise ValueError(f"8-bit row shapes disagree: codes {tuple(self.codes.shape)}, "
-                             f"scale {tuple(self.scale.shape)}")
+        codes, scale = self.codes, self.scale
+        dev = _device_of(codes)
+        _plain(codes, torch.int8 if codes.dtype == torch.int8 else torch.uint8, "codes", dev)
+        _plain(scale, torch.float32, "scale", dev)
+        shape = codes.shape
+        if len(shape) != 2 or scale.shape != shape[:1]:
+            raise ValueError(f"8-bit row shapes disagree: codes {tuple(shape)}, scale {tuple(scale.shape)}")
 
     def dequant(self) -> torch.Tensor:
         """The float32 values [M, K] the rows stand for."""
@@ -69,24 +71,32 @@ def _device_of(t) -> int:
     return torch.cuda.current_device() if isinstance(t, torch.Tensor) and t.is_cuda else -2
 
 
-def _plain(t, dtype, name: str, dev: int):
-    """A contiguous device tensor of a type (as _need, which words the refusals)."""
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.get_device() == dev and t.is_contiguous()):
-        _need(t, dtype, name)
+def _plain(t, dtype, name: str, dev: int) -> int:
+    """The pointer of a contiguous device tensor of a type (_need words the refusals)."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, dtype, name)
     return t.data_ptr()
 
 
 def _rows(t, name: str, dev: int, shape=None, dtype=None) -> int:
     """Checks a [M, K] tensor whose rows may be strided; returns the row stride."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in _DTYPES if dtype is None else t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype or 'float32, float16 or bfloat16'}, got {t.dtype}")
+    try:
+        have, kind = t.shape, t.dtype
+        if have == shape and t.is_contiguous() and t.get_device() == dev and \
+                (kind is dtype or dtype is None and kind in _DTYPES):
+            return have[1]
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    if kind not in _DTYPES if dtype is None else kind != dtype:
+        raise TypeError(f"{name} must be {dtype or 'float32, float16 or bfloat16'}, got {kind}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
     if t.get_device() != dev:
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a device tensor")
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
-    have = t.shape
     if len(have) != 2 or (shape is not None and have != shape):
         raise ValueError(f"{name} must be {'[M, K]' if shape is None else list(shape)}, got {list(have)}")
     M, K = have
@@ -218,22 +228,26 @@ def _pack(x: A8Rows, w, y: torch.Tensor, bias, dev: int, known: A8Rows | None = 
         raise TypeError("x must be an A8Rows (quantize_rows, rms_norm or silu_mul with a format)")
     if not isinstance(w, (Q8Weight, F8Weight)):
         raise TypeError(f"8-bit rows multiply a Q8Weight or an F8Weight, got {type(w).__name__}")
-    codes, fmt = x.codes, w.fmt
-    if codes.dtype != _CODES[fmt]:
-        raise TypeError(f"{codes.dtype} rows do not multiply a {type(w).__name__}")
+    codes, payload, fmt = x.codes, w.payload, w.fmt
+    dtype = _CODES[fmt]
     if x is not known:
+        if codes.dtype != dtype:
+            raise TypeError(f"{codes.dtype} rows do not multiply a {type(w).__name__}")
         x.validate()
+    elif codes.dtype is not dtype:
+        raise TypeError(f"{codes.dtype} rows do not multiply a {type(w).__name__}")
     M, K = codes.shape
-    payload = w.payload
-    wp = _plain(payload, _CODES[fmt], "payload", dev)
-    if payload.dim() != 2 or payload.shape[1] != K:
-        raise ValueError(f"x is {list(codes.shape)}, the weight {list(payload.shape)}")
-    N = payload.shape[0]
+    wp = _plain(payload, dtype, "payload", dev)
+    shape = payload.shape
+    if len(shape) != 2 or shape[1] != K:
+        raise ValueError(f"x is {list(codes.shape)}, the weight {list(shape)}")
+    N = shape[0]
     sp = bp = 0
     if fmt == FMT_Q8:
-        sp = _plain(w.scale, torch.float32, "scale", dev)
-        if w.scale.shape != (N,):
-            raise ValueError(f"int8 weight shapes disagree: payload {list(payload.shape)}, scale {list(w.scale.shape)}")
+        scale = w.scale
+        sp = _plain(scale, torch.float32, "scale", dev)
+        if scale.shape != (N,):
+            raise ValueError(f"int8 weight shapes disagree: payload {list(shape)}, scale {list(scale.shape)}")
     ldy = _rows(y, "y", dev, (M, N))
     if bias is not None:
         bp = _plain(bias, torch.float32, "bias", dev)
