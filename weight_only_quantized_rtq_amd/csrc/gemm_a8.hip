@@ -86,19 +86,21 @@ __device__ __forceinline__ i32x4 drop_bytes(i32x4 v, int s) {
     return c;
 }
 
-// 16 bytes of a row of K at k, zeros past K. A chunk that the row ends in is
-// the row's last 16 bytes, shifted: one load without a branch.
+// 16 bytes of a row of K >= 16 at k, zeros past K. A chunk that the row ends
+// in is the row's last 16 bytes, shifted: one load without a branch.
 __device__ __forceinline__ i32x4 load16(const uint8_t* row, int k, int K) {
+    i32x4 v;
+    const int at = min(k, K - 16);
+    __builtin_memcpy(&v, row + at, 16);
+    return drop_bytes(v, k - at);
+}
+
+// The same for K < 16, byte by byte.
+__device__ __forceinline__ i32x4 load_bytes(const uint8_t* row, int k, int K) {
     i32x4 v = {0, 0, 0, 0};
-    if (K >= 16) {
-        const int at = min(k, K - 16);
-        __builtin_memcpy(&v, row + at, 16);
-        v = drop_bytes(v, k - at);
-    } else {
 #pragma unroll
-        for (int j = 0; j < 15; ++j)
-            if (k + j < K) v[j / 4] |= static_cast<int>(row[k + j]) << (8 * (j % 4));
-    }
+    for (int j = 0; j < 15; ++j)
+        if (k + j < K) v[j / 4] |= static_cast<int>(row[k + j]) << (8 * (j % 4));
     return v;
 }
 
@@ -213,7 +215,7 @@ __global__ __launch_bounds__(W * 64) void skinny_kernel(const A8Args args) {
                 if (at + g * 16 < K) __builtin_memcpy(&v, p + at, 16);
                 return v;
             } else {
-                return load16(p - g * 16, at + g * 16, K);
+                return K >= 16 ? load16(p - g * 16, at + g * 16, K) : load_bytes(p - g * 16, at + g * 16, K);
             }
         };
         const i32x4 a0 = last(w, k), a1 = last(w, k + 64);
@@ -299,7 +301,7 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(const A8Args args) {
     const int high = min(kBand, tiles_m - band * kBand);
     const int64_t m0 = static_cast<int64_t>(band * kBand + in_band % high) * BM;
     const int n0 = in_band / high * BN;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave % WM * (TM * 16), wn = wave / WM * (TN * 16);
     const int r16 = lane & 15, g = lane >> 4;
     const uint8_t* xb = t.x + m0 * K;
@@ -321,18 +323,33 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(const A8Args args) {
         off[j] = static_cast<uint32_t>(row < left ? row : static_cast<int>(left)) * static_cast<uint32_t>(K);
     }
     i32x4 hold[ALIGNED ? 1 : OPS];
-    auto issue = [&](int k0, int buf) {
+    auto issue = [&](int step, int buf) {
+        const int k0 = step * kBK;
+        const uint8_t *x0 = xb + k0, *w0 = wb + k0;
+        if (k0 + kBK <= K) {
 #pragma unroll
-        for (int j = 0; j < OPS; ++j) {
-            const uint8_t* base = j * NW * 8 < BM ? xb : wb;
-            const int chunk = j * NW * 8 < BM ? chunk_x : chunk_w;
-            if constexpr (ALIGNED) {
-                const uint8_t* src = base + k0 + (off[j] + chunk);
-                if (k0 + kBK > K && k0 + chunk >= K) src = reinterpret_cast<const uint8_t*>(zero_chunk);
-                dma16(src, &lds[buf][(j * NW + wave) * 1024]);
-            } else {
-                if (k0 + kBK <= K) __builtin_memcpy(&hold[j], base + off[j] + k0 + chunk, 16);
-                else hold[j] = load16(base + off[j], k0 + chunk, K);
+            for (int j = 0; j < OPS; ++j) {
+                const bool is_x = j * NW * 8 < BM;
+                const uint8_t* src = (is_x ? x0 : w0) + (off[j] + static_cast<uint32_t>(is_x ? chunk_x : chunk_w));
+                if constexpr (ALIGNED) dma16(src, &lds[buf][(j * NW + wave) * 1024]);
+                else {
+                    i32x4 v;
+                    __builtin_memcpy(&v, src, 16);
+                    hold[j] = v;
+                }
+            }
+        } else {                                               // the last stage: zeros past K
+#pragma unroll
+            for (int j = 0; j < OPS; ++j) {
+                const bool is_x = j * NW * 8 < BM;
+                const int chunk = is_x ? chunk_x : chunk_w;
+                const uint8_t* row = (is_x ? xb : wb) + off[j];
+                if constexpr (ALIGNED) {
+                    const uint8_t* src = k0 + chunk < K ? row + k0 + chunk : reinterpret_cast<const uint8_t*>(zero_chunk);
+                    dma16(src, &lds[buf][(j * NW + wave) * 1024]);
+                } else {
+                    hold[j] = load16(row, k0 + chunk, K);
+                }
             }
         }
     };
@@ -348,9 +365,10 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(const A8Args args) {
     const int steps = (K + kBK - 1) / kBK;
 #pragma unroll
     for (int j = 0; j < S - 1; ++j)
-        if (j < steps) issue(j * kBK, j);
+        if (j < steps) issue(j, j);
     settle(0);
-    for (int step = 0, buf = 0; step < steps; ++step, buf = buf + 1 < S ? buf + 1 : 0) {
+    auto stage = [&](int step, auto buf_c) {
+        constexpr int buf = decltype(buf_c)::value, ahead = (buf + S - 1) % S;
         if constexpr (ALIGNED) {
             // Nothing moves past here: the last stage's LDS reads are all
             // used, so complete, before the barrier that frees their buffer.
@@ -364,32 +382,43 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(const A8Args args) {
         } else {
             __syncthreads();
         }
-        const int ahead = buf > 0 ? buf - 1 : S - 1;           // (buf + S - 1) % S: the stage before this one's
         const bool more = step + S - 1 < steps;
-        if (more) issue((step + S - 1) * kBK, ahead);
         const uint8_t* xs = lds[buf] + wm * kBK;
         const uint8_t* ws = lds[buf] + (BM + wn) * kBK;
-        i32x4 b[TM][2];
+        i32x4 b[TM][2], a[TN][2];
+        auto read_a = [&](int i) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                a[i][h] = *reinterpret_cast<const i32x4*>(ws + lds_at<kWide>(n_row<kWide>(i, r16), g + 4 * h));
+        };
+        // Enough operands for the first products are on their way before the
+        // copies are issued (LDS reads do not move across those).
+        constexpr int kFirst = TN < 2 ? TN : 2;
 #pragma unroll
         for (int q = 0; q < TM; ++q)
 #pragma unroll
             for (int h = 0; h < 2; ++h) b[q][h] = *reinterpret_cast<const i32x4*>(xs + lds_at<true>(q * 16 + r16, g + 4 * h));
+#pragma unroll
+        for (int i = 0; i < kFirst; ++i) read_a(i);
+        if (more) issue(step + S - 1, ahead);
         // While one wave of a SIMD reads operands the other's matrix instructions
         // go first (8192^3 E4M3: 414 -> 409 us; with the bf16 conversions between
         // them it costs instead, 55.7 -> 66.7 us for 16384 x 2048 x 512).
         if constexpr (KIND != kA8F8Wide) __builtin_amdgcn_s_setprio(1);
-        i32x4 a[TN][2];
 #pragma unroll
-        for (int i = 0; i < TN; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                a[i][h] = *reinterpret_cast<const i32x4*>(ws + lds_at<kWide>(n_row<kWide>(i, r16), g + 4 * h));
+        for (int i = kFirst; i < TN; ++i) read_a(i);
 #pragma unroll
         for (int i = 0; i < TN; ++i)
 #pragma unroll
             for (int q = 0; q < TM; ++q) acc[i][q] = mma<KIND>(a[i][0], a[i][1], b[q][0], b[q][1], acc[i][q]);
         if constexpr (KIND != kA8F8Wide) __builtin_amdgcn_s_setprio(0);
         if (more) settle(ahead);
+    };
+    for (int step = 0; step < steps; step += S) {              // buffers by constant numbers
+        stage(step, std::integral_constant<int, 0>());
+        if constexpr (S > 1) { if (step + 1 < steps) stage(step + 1, std::integral_constant<int, 1 % S>()); }
+        if constexpr (S > 2) { if (step + 2 < steps) stage(step + 2, std::integral_constant<int, 2 % S>()); }
+        if constexpr (S > 3) { if (step + 3 < steps) stage(step + 3, std::integral_constant<int, 3 % S>()); }
     }
 
     // Lane: m = lane % 16 of each block q; C adjacent n of each group of
@@ -477,22 +506,23 @@ hipError_t launch_kind(A8Args& args, hipStream_t stream) {
     // Larger blocks read less, smaller ones keep 256 CUs busy: by the call's
     // count of blocks of each size. us, int8 to bf16, M x N x K, as graph
     // replays (the count in brackets):
-    //   16 x 16 straight to registers / 32 x 64 tiles: 80 x 512 x 512 (160) 3.3 / 4.1;
-    //     64 x 2048 x 8192 (512) 13.9 / 22.6; 128 x 2048 x 512 (1024) 4.4 / 4.1
-    //   one / two blocks of m a wave: 64 x 512 x 8192 (128) 10.0 / 13.5; 64 x 2048 x 8192 (512) 17.4 / 13.9
-    //   32 x 64 / 64 x 64: 512 x 2048 x 2048 (512) 9.2 / 9.4; 700 x 2048 x 8192 (704) 32.0 / 28.7
-    //   64 x 64 / 128 x 128: 1024 x 2048 x 8192 (512) 29.8 / 40.8; 1500 x 2048 x 8192 (768) 56.2 / 44.8
+    //   16 x 16 straight to registers / 32 x 64 tiles: 80 x 512 x 512 (160) 3.3 / 3.8;
+    //     64 x 2048 x 8192 (512) 13.8 / 14.3; 80 x 2048 x 2048 (640) 7.5 / 5.7
+    //   one / two blocks of m a wave: 64 x 512 x 8192 (128) 9.8 / 13.3; 64 x 2048 x 8192 (512) 17.4 / 13.8
+    //   32 x 64 / 64 x 64: 700 x 512 x 2048 (176) 6.3 / 7.2; 700 x 2048 x 8192 (704) 29.2 / 25.6
+    //   64 x 64 / 128 x 128: 1500 x 512 x 8192 (192) 18.6 / 33.4; 1500 x 2048 x 8192 (768) 43.6 / 36.5
     //   128 x 128 of eight waves and four stages, one a CU / of four waves and
-    //     two stages, two a CU: 2048 x 2048 x 8192 (256) 43.0 / 47.7; 3000 x 2048 x 8192 (384) 83.4 / 54.9
-    //   128 x 128 / 256 x 256: a round of 512 takes 0.57 of a round of 256 of
-    //     the large ones (63.6 us and 111.6 us at K = 8192)
+    //     two stages, two a CU: 1500 x 2048 x 8192 (192) 36.5 / 46.2; 3000 x 2048 x 8192 (384) 70.5 / 55.3
+    //   128 x 128 / 256 x 256: a round of 512 takes 4/7 of a round of 256 of
+    //     the large ones: 1500 x 8192 x 8192 (768, 192) 106.6 / 94.0; 3000 x 8192 x 8192 (1536, 384) 188.7 / 195.9
     // Rows through registers (two stages only): 16 x 16 / 32 x 64: 77 x 513 x
-    // 2053 (165) 8.3 / 12.5, 250 x 513 x 515 (528) 8.0 / 6.6; 32 x 64 / 64 x
-    // 64: 515 x 2051 x 2053 (561) 21.5 / 23.1, 1030 x 2051 x 2053 (1089) 29.7 / 27.6.
+    // 2053 (165) 8.2 / 11.3, 250 x 513 x 515 (528) 8.0 / 6.1.
     const int64_t n16 = number(args, 16, 16);
-    if (args.M <= 16) return skinny(c1, c8);
-    if (n16 <= (ALIGNED ? 600 : 300)) return n16 < 384 ? skinny(c1, c8) : skinny(c2, c8);
-    if (number(args, 32, 64) <= (ALIGNED ? 512 : 768)) return tiles(c32, c64, c2, c2, c4);
+    bool short_k = false;                                      // the tiles load 16 bytes of a row at a time
+    for (int j = 0; j < args.count; ++j) short_k |= args.task[j].K < 16;
+    if (args.M <= 16 || short_k) return skinny(c1, c8);
+    if (n16 <= (ALIGNED ? 512 : 300)) return n16 < 384 ? skinny(c1, c8) : skinny(c2, c8);
+    if (number(args, 32, 64) <= 512) return tiles(c32, c64, c2, c2, c4);
     if (number(args, 64, 64) <= 512) return tiles(c64, c64, c2, c2, c4);
     const int64_t n128 = number(args, 128, 128), n256 = number(args, 256, 256);
     if (n128 <= 256) return tiles(c128, c128, c4, c2, c4);
