@@ -363,8 +363,11 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(const A8Args args) {
 
     typename Acc<KIND>::T acc[TN][TM] = {};
     const int steps = (K + kBK - 1) / kBK;
+    // Every buffer is free at the start, so S stages are on their way; from the
+    // second step on each step issues the one that its predecessor made room for.
+    constexpr int kStart = ALIGNED ? S : 1;
 #pragma unroll
-    for (int j = 0; j < S - 1; ++j)
+    for (int j = 0; j < kStart; ++j)
         if (j < steps) issue(j, j);
     settle(0);
     auto stage = [&](int step, auto buf_c) {
@@ -373,16 +376,18 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(const A8Args args) {
             // Nothing moves past here: the last stage's LDS reads are all
             // used, so complete, before the barrier that frees their buffer.
             __builtin_amdgcn_sched_barrier(0);
-            // This wave's part of the stage: the S - 2 stages issued after it
-            // may stay in flight (near the end there are fewer: wait for all).
-            if (S == 2 || step + S - 1 > steps) wait_vm<0>();
+            // This wave's part of the stage. The stages issued after it may stay
+            // in flight: S - 2 of them, at the first step S - 1 (with fewer
+            // steps left than that, wait for all).
+            if (step == 0 && steps >= S) wait_vm<(S - 1) * OPS>();
+            else if (S == 2 || step + S - 1 > steps) wait_vm<0>();
             else wait_vm<(S - 2) * OPS>();
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
         } else {
             __syncthreads();
         }
-        const bool more = step + S - 1 < steps;
+        const bool more = step + S - 1 < steps && (!ALIGNED || step > 0);
         const uint8_t* xs = lds[buf] + wm * kBK;
         const uint8_t* ws = lds[buf] + (BM + wn) * kBK;
         i32x4 b[TM][2], a[TN][2];
