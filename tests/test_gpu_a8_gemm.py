@@ -309,3 +309,31 @@ def test_refusals_on_the_device():
     other, _, _ = dev(*make(5, 64, 128, "q8", 1))
     with pytest.raises(ValueError, match="share M"):
         rtq.project_a8([rtq.Projection(w, x, y), rtq.Projection(w, other, torch.empty(5, 64, device=DEV))])
+
+
+def test_more_columns_than_one_launch_holds():
+    """N past the columns of one launch, alone and beside a small task; the pieces meet at column 2^23."""
+    N, K = (1 << 23) + 37, 16
+    g = torch.Generator(device=DEV).manual_seed(8)
+    w = rtq.Q8Weight(torch.randint(-127, 128, (N, K), generator=g, device=DEV, dtype=torch.int8),
+                     torch.rand(N, generator=g, device=DEV))
+    bias = torch.rand(N, generator=g, device=DEV)
+    x, small, _ = dev(*make(2, 50, K, "q8", 9))
+    y, y2 = torch.full((2, N), float("nan"), device=DEV), torch.empty(2, 50, device=DEV)
+    rtq.project_a8([rtq.Projection(w, x, y, bias), rtq.Projection(small, x, y2)])
+    check(y2, x, small, None)
+    for at in (0, (1 << 23) - 40, N - 64):
+        part = slice(at, min(N, at + 77))
+        check(y[:, part], x, rtq.Q8Weight(w.payload[part], w.scale[part]), bias[part])
+    assert not torch.isnan(y).any()
+
+
+def test_timing_marks_cover_the_product():
+    x, w, _ = dev(*make(80, 64, 128, "q8", 1))
+    rtq.timing_enable(True)
+    try:
+        rtq.gemm_a8(x, w)
+        ms, launches = rtq.timing_read()
+    finally:
+        rtq.timing_enable(False)
+    assert launches == 1 and ms > 0

@@ -254,3 +254,52 @@ def test_refusals_on_the_device():
         rtq.quantize_rows(x, "f8", out=rtq.A8Rows(torch.empty(4, 64, dtype=torch.int8, device=DEV), w[:4]))
     with pytest.raises(ValueError):
         rtq.quantize_rows(x, "q8", out=rtq.A8Rows(torch.empty(4, 63, dtype=torch.int8, device=DEV), w[:4]))
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 elements: rows at the far ends against the same rows on their own."""
+    M, K = (1 << 20) + 700, 4104
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device=DEV)
+    ends = torch.tensor([0, 1, (1 << 32) // K - 1, (1 << 32) // K, (1 << 32) // K + 1, M - 1], device=DEV)
+    x[ends] = torch.randn(len(ends), K, device=DEV).to(torch.bfloat16)
+    w = torch.rand(K, device=DEV)
+    few = x[ends].contiguous()
+    for fmt in ("q8", "f8"):
+        for call in (lambda v: rtq.quantize_rows(v, fmt), lambda v: rtq.rms_norm(v, w, fmt=fmt),
+                     lambda v: rtq.silu_mul(v, v, fmt=fmt)):
+            big, want = call(x), call(few)
+            assert torch.equal(big.codes[ends], want.codes) and torch.equal(big.scale[ends], want.scale)
+            assert big.scale.count_nonzero() == len(ends)
+            del big
+
+
+@pytest.mark.parametrize("fmt", ["q8", "f8", None])
+def test_captured_and_on_other_streams(fmt):
+    """Two streams at once, and a graph replayed with new inputs and eager work in between."""
+    g = torch.Generator().manual_seed(3)
+    xs = [torch.randn(33, 1000, generator=g).to(DEV) for _ in range(4)]
+    res, w = torch.randn(33, 1000, generator=g).to(DEV), torch.rand(1000, generator=g).to(DEV)
+
+    def values(r):
+        out, h = r
+        return [h] + ([out] if fmt is None else [out.codes, out.scale])
+
+    want = [values(rtq.rms_norm(x, w, residual=res, fmt=fmt)) for x in xs]
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in range(2)]
+    got = [values(rtq.rms_norm(x, w, residual=res, fmt=fmt, stream=side[i % 2])) for i, x in enumerate(xs)]
+    raw = values(rtq.rms_norm(xs[0], w, residual=res, fmt=fmt, stream=side[0].cuda_stream))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for r, s in zip(got, want) for a, b in zip(r, s))
+    assert all(torch.equal(a, b) for a, b in zip(raw, want[0]))
+    x = xs[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = values(rtq.rms_norm(x, w, residual=res, fmt=fmt))
+    for i in (2, 1, 3, 0):
+        x.copy_(xs[i])
+        graph.replay()
+        eager = values(rtq.rms_norm(xs[(i + 1) % 4], w, residual=res, fmt=fmt))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
+        assert all(torch.equal(a, b) for a, b in zip(eager, want[(i + 1) % 4]))

@@ -68,7 +68,7 @@ class A8Rows:
 def _device_of(t) -> int:
     """The device of a call: the current one, which every tensor has to be on.
     What is no device tensor is refused by its own check, without asking for one."""
-    return torch.cuda.current_device() if isinstance(t, torch.Tensor) and t.is_cuda else -2
+    return torch._C._cuda_getDevice() if isinstance(t, torch.Tensor) and t.is_cuda else -2
 
 
 def _plain(t, dtype, name: str, dev: int) -> int:

@@ -544,29 +544,45 @@ bool task_aligned(const A8Task& t) {
 }  // namespace
 
 hipError_t launch_a8(const A8Task* tasks, int count, int64_t M, hipStream_t stream) {
-    // Rows of one launch: its tiles stay below 2^23 whatever N is (a grid
-    // holds fewer than 2^32 threads).
-    constexpr int64_t kMaxTiles = int64_t(1) << 23;
+    // A grid holds fewer than 2^32 threads: one launch covers at most 2^22 of
+    // the smallest blocks (16 x 16, 512 threads), so wide tasks go in pieces
+    // of columns and tall ones in pieces of rows.
+    constexpr int64_t kMaxBlocks = int64_t(1) << 22;
+    constexpr int kMaxCols = static_cast<int>(kMaxBlocks / kA8Slots * 16);
     A8Args args;
     // One launch holds tasks of one kind, and of one of the two ways to load.
     for (int pass = 0; pass < kA8Kinds * 2; ++pass) {
         const int kind = pass / 2;
         const bool whole = pass % 2 == 0;
-        for (int at = 0; at < count;) {
-            int64_t tiles_n = 0;
-            const A8Task* slot[kA8Slots];
+        int at = 0, col = 0;                                   // the next task and its first column
+        while (at < count) {
+            int64_t blocks_n = 0;
+            A8Task slot[kA8Slots];
             args.count = 0;
-            for (; at < count && args.count < kA8Slots; ++at) {
-                if (tasks[at].kind != kind || task_aligned(tasks[at]) != whole) continue;
-                slot[args.count++] = &tasks[at];
-                tiles_n += (tasks[at].N + 15) / 16;
+            while (at < count && args.count < kA8Slots) {
+                if (tasks[at].kind != kind || task_aligned(tasks[at]) != whole) {
+                    ++at;
+                    continue;
+                }
+                A8Task& t = slot[args.count++] = tasks[at];
+                t.w += static_cast<int64_t>(col) * t.K;
+                if (t.w_scale) t.w_scale += col;
+                if (t.bias) t.bias += col;
+                t.y = static_cast<uint8_t*>(t.y) + static_cast<int64_t>(col) * (t.y_dtype == RTQ_F32 ? 4 : 2);
+                t.N = t.N - col < kMaxCols ? t.N - col : kMaxCols;
+                col += t.N;
+                if (col >= tasks[at].N) {
+                    ++at;
+                    col = 0;
+                }
+                blocks_n += (t.N + 15) / 16;
             }
             if (!args.count) break;
-            const int64_t most = kMaxTiles / tiles_n > 0 ? kMaxTiles / tiles_n * 16 : 16;
+            const int64_t most = kMaxBlocks / blocks_n * 16;   // rows of a launch
             for (int64_t m = 0; m < M; m += most) {
                 args.M = M - m < most ? M - m : most;
                 for (int j = 0; j < args.count; ++j) {
-                    A8Task& t = args.task[j] = *slot[j];
+                    A8Task& t = args.task[j] = slot[j];
                     t.x += m * t.K;
                     t.x_scale += m;
                     t.y = static_cast<uint8_t*>(t.y) + m * t.ldy * (t.y_dtype == RTQ_F32 ? 4 : 2);
@@ -575,10 +591,12 @@ hipError_t launch_a8(const A8Task* tasks, int count, int64_t M, hipStream_t stre
                     constexpr int KIND = decltype(k)::value;
                     return whole ? launch_kind<KIND, true>(args, stream) : launch_kind<KIND, false>(args, stream);
                 };
+                const int mark = timing_begin(stream);
                 const hipError_t e = kind == kA8Int       ? run(std::integral_constant<int, kA8Int>())
                                      : kind == kA8IntWide ? run(std::integral_constant<int, kA8IntWide>())
                                      : kind == kA8F8      ? run(std::integral_constant<int, kA8F8>())
                                                           : run(std::integral_constant<int, kA8F8Wide>());
+                timing_end(mark, stream);
                 if (e != hipSuccess) return e;
             }
         }
