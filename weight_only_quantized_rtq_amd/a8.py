@@ -25,6 +25,10 @@ from . import FMT_F8, FMT_NONE, FMT_Q8, MAX_BLOCKS, F8Weight, Projection, Q8Weig
 A8_MAX_K = 131071
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _FMTS = {None: FMT_NONE, "q8": FMT_Q8, "f8": FMT_F8}
+_Tensor = torch.Tensor
+# what torch.cuda.current_device() and current_stream().cuda_stream come down to, where torch has a GPU
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 _CODES = {FMT_Q8: torch.int8, FMT_F8: torch.uint8}
 
 
@@ -68,7 +72,7 @@ class A8Rows:
 def _device_of(t) -> int:
     """The device of a call: the current one, which every tensor has to be on.
     What is no device tensor is refused by its own check, without asking for one."""
-    return torch._C._cuda_getDevice() if isinstance(t, torch.Tensor) and t.is_cuda else -2
+    return _current_device() if isinstance(t, _Tensor) and t.is_cuda else -2
 
 
 def _plain(t, dtype, name: str, dev: int) -> int:
@@ -86,8 +90,9 @@ def _rows(t, name: str, dev: int, shape=None, dtype=None) -> int:
     """Checks a [M, K] tensor whose rows may be strided; returns the row stride."""
     try:
         have, kind = t.shape, t.dtype
-        if have == shape and t.is_contiguous() and t.get_device() == dev and \
-                (kind is dtype or dtype is None and kind in _DTYPES):
+        if t.is_contiguous() and t.get_device() == dev and \
+                (kind in _DTYPES if dtype is None else kind is dtype) and \
+                (len(have) == 2 if shape is None else have == shape):
             return have[1]
     except AttributeError:
         raise TypeError(f"{name} must be a torch.Tensor") from None
@@ -112,7 +117,7 @@ def _rows(t, name: str, dev: int, shape=None, dtype=None) -> int:
 
 def _launch_stream(stream, dev: int) -> int:
     """The raw stream of the call: the device's current one, or the given one."""
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    return _current_stream(dev) if stream is None else _stream(stream)
 
 
 def _on(stream):
@@ -230,12 +235,10 @@ def _pack(x: A8Rows, w, y: torch.Tensor, bias, dev: int, known: A8Rows | None = 
         raise TypeError(f"8-bit rows multiply a Q8Weight or an F8Weight, got {type(w).__name__}")
     codes, payload, fmt = x.codes, w.payload, w.fmt
     dtype = _CODES[fmt]
-    if x is not known:
-        if codes.dtype != dtype:
-            raise TypeError(f"{codes.dtype} rows do not multiply a {type(w).__name__}")
-        x.validate()
-    elif codes.dtype is not dtype:
+    if codes.dtype is not dtype:
         raise TypeError(f"{codes.dtype} rows do not multiply a {type(w).__name__}")
+    if x is not known:
+        x.validate()
     M, K = codes.shape
     wp = _plain(payload, dtype, "payload", dev)
     shape = payload.shape
