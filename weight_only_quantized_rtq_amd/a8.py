@@ -227,23 +227,32 @@ def silu_mul(a: torch.Tensor, b: torch.Tensor, fmt: str | None = None, out=None,
     return out
 
 
-def _pack(x: A8Rows, w, y: torch.Tensor, bias, dev: int, known: A8Rows | None = None) -> bytes:
-    """One checked descriptor. `known` is rows of this call that are checked already."""
+def _not_a_weight(w) -> TypeError:
+    return TypeError(f"8-bit rows multiply a Q8Weight or an F8Weight, got {type(w).__name__}")
+
+
+def _checked(x: A8Rows):
+    """Rows of a call, checked: (fmt, M, K, the codes' pointer, the scales')."""
     if not isinstance(x, A8Rows):
         raise TypeError("x must be an A8Rows (quantize_rows, rms_norm or silu_mul with a format)")
-    if not isinstance(w, (Q8Weight, F8Weight)):
-        raise TypeError(f"8-bit rows multiply a Q8Weight or an F8Weight, got {type(w).__name__}")
-    codes, payload, fmt = x.codes, w.payload, w.fmt
-    dtype = _CODES[fmt]
-    if codes.dtype is not dtype:
-        raise TypeError(f"{codes.dtype} rows do not multiply a {type(w).__name__}")
-    if x is not known:
-        x.validate()
+    x.validate()
+    codes = x.codes
     M, K = codes.shape
-    wp = _plain(payload, dtype, "payload", dev)
+    return x.fmt, M, K, codes.data_ptr(), x.scale.data_ptr()
+
+
+def _pack(rows, w, y: torch.Tensor, bias, dev: int) -> bytes:
+    """One descriptor; `rows` is what _checked() gave."""
+    if not isinstance(w, (Q8Weight, F8Weight)):
+        raise _not_a_weight(w)
+    x_fmt, M, K, xp, xsp = rows
+    payload, fmt = w.payload, w.fmt
+    if fmt != x_fmt:
+        raise TypeError(f"{_CODES[x_fmt]} rows do not multiply a {type(w).__name__}")
+    wp = _plain(payload, _CODES[fmt], "payload", dev)
     shape = payload.shape
     if len(shape) != 2 or shape[1] != K:
-        raise ValueError(f"x is {list(codes.shape)}, the weight {list(shape)}")
+        raise ValueError(f"x is [{M}, {K}], the weight {list(shape)}")
     N = shape[0]
     sp = bp = 0
     if fmt == FMT_Q8:
@@ -256,7 +265,7 @@ def _pack(x: A8Rows, w, y: torch.Tensor, bias, dev: int, known: A8Rows | None = 
         bp = _plain(bias, torch.float32, "bias", dev)
         if bias.shape != (N,):
             raise ValueError(f"bias {list(bias.shape)} does not match N={N}")
-    return _PROJ_A8.pack(fmt, N, K, _DTYPES[y.dtype], codes.data_ptr(), x.scale.data_ptr(), wp, sp, y.data_ptr(), ldy, bp)
+    return _PROJ_A8.pack(fmt, N, K, _DTYPES[y.dtype], xp, xsp, wp, sp, y.data_ptr(), ldy, bp)
 
 
 def gemm_a8(x: A8Rows, w, y: torch.Tensor | None = None, bias: torch.Tensor | None = None, out_dtype=None,
@@ -264,19 +273,21 @@ def gemm_a8(x: A8Rows, w, y: torch.Tensor | None = None, bias: torch.Tensor | No
     """y = x . W^T (+ bias) for 8-bit rows and a Q8Weight or F8Weight of the same
     format (rtq_gemm_a8). y is float32 unless out_dtype (or y itself) says otherwise."""
     lib = load_library()
+    if not isinstance(w, (Q8Weight, F8Weight)):
+        raise _not_a_weight(w)
     if y is None:
-        if not isinstance(x, A8Rows):
-            raise TypeError("x must be an A8Rows (quantize_rows, rms_norm or silu_mul with a format)")
         out_dtype = torch.float32 if out_dtype is None else out_dtype
         if out_dtype not in _DTYPES:
             raise TypeError(f"out_dtype must be float32, float16 or bfloat16, got {out_dtype}")
+    rows = _checked(x)
+    if y is None:
         with _on(stream):
-            y = torch.empty((x.M, w.N), dtype=out_dtype, device=x.codes.device)
+            y = torch.empty((rows[1], w.N), dtype=out_dtype, device=x.codes.device)
     elif out_dtype not in (None, y.dtype):
         raise TypeError(f"y is {y.dtype}, out_dtype {out_dtype}")
     dev = _device_of(y)
-    d = _pack(x, w, y, bias, dev)
-    _check(lib.rtq_gemm_a8(d, y.shape[0], _launch_stream(stream, dev)))
+    d = _pack(rows, w, y, bias, dev)
+    _check(lib.rtq_gemm_a8(d, rows[1], _launch_stream(stream, dev)))
     return y
 
 
@@ -289,12 +300,12 @@ def project_a8(projections: list[Projection], stream=None) -> None:
         raise ValueError(f"1..{MAX_BLOCKS * 8} projections per call, got {len(projections)}")
     dev, known, M, packed = _device_of(projections[0].y), None, None, []
     for p in projections:
-        packed.append(_pack(p.x, p.weight, p.y, p.bias, dev, known))
         if p.x is not known:
-            known = p.x
-            if M not in (None, known.M):
-                raise ValueError(f"the projections of one call share M: {known.M} and {M}")
-            M = known.M
+            known, rows = p.x, _checked(p.x)
+            if M not in (None, rows[1]):
+                raise ValueError(f"the projections of one call share M: {rows[1]} and {M}")
+            M = rows[1]
+        packed.append(_pack(rows, p.weight, p.y, p.bias, dev))
     _check(lib.rtq_project_a8(b"".join(packed), len(packed), M, _launch_stream(stream, dev)))
 
 
@@ -304,7 +315,7 @@ def ffn_a8(x: torch.Tensor, weight: torch.Tensor, w1, w3, w2, eps: float = 1e-6,
     (silu(n . W1^T) * (n . W3^T)) . W2^T, every product on 8-bit rows of the
     weights' format. Returns y [M, w2.N] in x's dtype, or (y, x + residual)."""
     if not isinstance(w1, (Q8Weight, F8Weight)):
-        raise TypeError(f"8-bit rows multiply a Q8Weight or an F8Weight, got {type(w1).__name__}")
+        raise _not_a_weight(w1)
     fmt = "q8" if w1.fmt == FMT_Q8 else "f8"
     rows = rms_norm(x, weight, eps, residual=residual, fmt=fmt, stream=stream)
     h = None
