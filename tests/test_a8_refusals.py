@@ -162,7 +162,8 @@ def test_binding_refuses_host_tensors_and_types():
     x, w = torch.zeros(4, 128), torch.ones(128)
     q8 = rtq.Q8Weight(torch.zeros(64, 128, dtype=torch.int8), torch.zeros(64))
     for call in (lambda: rtq.quantize_rows(x), lambda: rtq.rms_norm(x, w), lambda: rtq.silu_mul(x, x),
-                 lambda: rtq.gemm_a8(rows(), q8), lambda: rtq.ffn_a8(x, w, q8, q8, q8)):
+                 lambda: rtq.gemm_a8(rows(), q8),
+                 lambda: rtq.ffn_a8(x, w, q8, q8, rtq.Q8Weight(torch.zeros(128, 64, dtype=torch.int8), torch.zeros(128)))):
         with pytest.raises(ValueError, match="device tensor"):
             call()
     with pytest.raises(TypeError):
@@ -179,6 +180,11 @@ def test_binding_refuses_host_tensors_and_types():
         rtq.gemm_a8(rows(), rtq.Q4Weight(torch.zeros(64, 64, dtype=torch.uint8), torch.zeros(64, 4, 2).half()))
     with pytest.raises(TypeError, match="Q4Weight"):
         rtq.ffn_a8(x, w, rtq.Q4Weight(torch.zeros(64, 64, dtype=torch.uint8), torch.zeros(64, 4, 2).half()), q8, q8)
+    with pytest.raises(ValueError, match="disagree"):
+        rtq.ffn_a8(x, w, q8, q8, rtq.Q8Weight(torch.zeros(128, 60, dtype=torch.int8), torch.zeros(128)))
+    f8 = rtq.F8Weight(torch.zeros(64, 128, dtype=torch.uint8))
+    with pytest.raises(TypeError, match="share a format"):
+        rtq.ffn_a8(x, w, q8, f8, q8)
     with pytest.raises(ValueError):
         rtq.project_a8([])
     with pytest.raises(TypeError, match="out_dtype"):

@@ -314,8 +314,13 @@ def ffn_a8(x: torch.Tensor, weight: torch.Tensor, w1, w3, w2, eps: float = 1e-6,
     """A gated FFN on 8-bit rows: with n = rms_norm(x (+ residual), weight),
     (silu(n . W1^T) * (n . W3^T)) . W2^T, every product on 8-bit rows of the
     weights' format. Returns y [M, w2.N] in x's dtype, or (y, x + residual)."""
-    if not isinstance(w1, (Q8Weight, F8Weight)):
-        raise _not_a_weight(w1)
+    for w in (w1, w3, w2):
+        if not isinstance(w, (Q8Weight, F8Weight)):
+            raise _not_a_weight(w)
+        if w.fmt != w1.fmt:
+            raise TypeError("the weights of one FFN share a format")
+    if (w3.N, w3.K, w2.K) != (w1.N, w1.K, w1.N):
+        raise ValueError(f"FFN weight shapes disagree: w1 [{w1.N}, {w1.K}], w3 [{w3.N}, {w3.K}], w2 [{w2.N}, {w2.K}]")
     fmt = "q8" if w1.fmt == FMT_Q8 else "f8"
     rows = rms_norm(x, weight, eps, residual=residual, fmt=fmt, stream=stream)
     h = None
