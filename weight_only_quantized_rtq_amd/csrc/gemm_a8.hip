@@ -95,7 +95,22 @@ __device__ __forceinline__ i32x4 load16(const uint8_t* row, int k, int K) {
     return drop_bytes(v, k - at);
 }
 
-// The same for K < 16, byte by byte.
+// 16 bytes at any address, from the aligned words that hold them. Each word
+// holds at least one of the 16 bytes, so none lies outside the tensor's words.
+__device__ __forceinline__ i32x4 load_words(const uint8_t* p) {
+    typedef int W4 __attribute__((ext_vector_type(4), aligned(4)));
+    const uint32_t r = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 3u;
+    const W4 v = *reinterpret_cast<const W4*>(p - r);
+    const int last = *reinterpret_cast<const int*>(p + (15u - ((r + 15u) & 3u)));
+    i32x4 o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        o[j] = static_cast<int>(__builtin_amdgcn_alignbyte(static_cast<uint32_t>(j < 3 ? v[j + 1] : last),
+                                                           static_cast<uint32_t>(v[j]), r));
+    return o;
+}
+
+// load16 for K < 16, byte by byte.
 __device__ __forceinline__ i32x4 load_bytes(const uint8_t* row, int k, int K) {
     i32x4 v = {0, 0, 0, 0};
 #pragma unroll
@@ -196,18 +211,25 @@ __global__ __launch_bounds__(W * 64) void skinny_kernel(const A8Args args) {
     }
     V acc[MT] = {};
     int k = wave * kBK;
-    for (; k + kBK <= K; k += W * kBK) {
-        i32x4 a0, a1;
-        __builtin_memcpy(&a0, w + k, 16);
-        __builtin_memcpy(&a1, w + k + 64, 16);
+    auto whole_steps = [&](auto load) {
+        for (; k + kBK <= K; k += W * kBK) {
+            const i32x4 a0 = load(w + k), a1 = load(w + k + 64);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            i32x4 b0, b1;
-            __builtin_memcpy(&b0, x[i] + k, 16);
-            __builtin_memcpy(&b1, x[i] + k + 64, 16);
-            acc[i] = mma<KIND>(a0, a1, b0, b1, acc[i]);
+            for (int i = 0; i < MT; ++i) acc[i] = mma<KIND>(a0, a1, load(x[i] + k), load(x[i] + k + 64), acc[i]);
         }
-    }
+    };
+    // Rows off the words go through words: 80 x 512 x 2049 takes 6.3 us, 10.4
+    // with loads at the bytes' own addresses. Rows on the words take those
+    // addresses: 80 x 512 x 2056 takes 4.3 us, 5.2 through words.
+    if (!ALIGNED && ((static_cast<uint32_t>(K) | static_cast<uint32_t>(reinterpret_cast<uintptr_t>(t.x)) |
+                      static_cast<uint32_t>(reinterpret_cast<uintptr_t>(t.w))) & 3u))
+        whole_steps([](const uint8_t* p) { return load_words(p); });
+    else
+        whole_steps([](const uint8_t* p) {
+            i32x4 v;
+            __builtin_memcpy(&v, p, 16);
+            return v;
+        });
     if (k < K) {                                               // the last, partial step
         auto last = [&](const uint8_t* p, int at) {            // p is 16 g into its row
             if constexpr (ALIGNED) {
@@ -520,13 +542,13 @@ hipError_t launch_kind(A8Args& args, hipStream_t stream) {
     //     two stages, two a CU: 1500 x 2048 x 8192 (192) 36.5 / 46.2; 3000 x 2048 x 8192 (384) 70.5 / 55.3
     //   128 x 128 / 256 x 256: a round of 512 takes 4/7 of a round of 256 of
     //     the large ones: 1500 x 8192 x 8192 (768, 192) 106.6 / 94.0; 3000 x 8192 x 8192 (1536, 384) 188.7 / 195.9
-    // Rows through registers (two stages only): 16 x 16 / 32 x 64: 77 x 513 x
-    // 2053 (165) 8.2 / 11.3, 250 x 513 x 515 (528) 8.0 / 6.1.
+    // The same where rows are not 16-byte aligned: 16 x 16 / 32 x 64: 200 x 512 x 2049
+    // (416) 8.3 / 10.6; 300 x 512 x 2049 (608) 12.5 / 10.6.
     const int64_t n16 = number(args, 16, 16);
     bool short_k = false;                                      // the tiles load 16 bytes of a row at a time
     for (int j = 0; j < args.count; ++j) short_k |= args.task[j].K < 16;
     if (args.M <= 16 || short_k) return skinny(c1, c8);
-    if (n16 <= (ALIGNED ? 512 : 300)) return n16 < 384 ? skinny(c1, c8) : skinny(c2, c8);
+    if (n16 <= 512) return n16 < 384 ? skinny(c1, c8) : skinny(c2, c8);
     if (number(args, 32, 64) <= 512) return tiles(c32, c64, c2, c2, c4);
     if (number(args, 64, 64) <= 512) return tiles(c64, c64, c2, c2, c4);
     const int64_t n128 = number(args, 128, 128), n256 = number(args, 256, 256);
