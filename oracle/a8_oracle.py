@@ -1,8 +1,9 @@
 """CPU oracle of the operators on 8-bit activations, in fp64 numpy.
 
 A row of values r * p_k gets codes rnd(R p_k / P), P = max|p|, nearest code with
-ties to even, R = 127 (int8) or 448 (E4M3), and the scale fp32(r P / R). Rows
-of zeros: scale 0, codes 0. Rows with an infinity or NaN, or a scale past
+ties to even, R = 127 (int8) or 448 (E4M3), and the scale fp32(r P / R). The
+fp64 quotient is rounded to 47 bits first, so that a true tie whose p and P are
+themselves rounded is a tie. Rows of zeros: scale 0, codes 0. Rows with an infinity or NaN, or a scale past
 fp32: scale NaN, codes 0.
 """
 from __future__ import annotations
@@ -25,6 +26,11 @@ def nearest_e4m3(t: np.ndarray) -> np.ndarray:
     return (code | (np.signbit(t).astype(np.int64) << 7)).astype(np.uint8)
 
 
+def to_47_bits(t: np.ndarray) -> np.ndarray:
+    """fp64 values rounded to 47 significant bits, halves away from zero."""
+    return ((t.view(np.uint64) + np.uint64(32)) & ~np.uint64(63)).view(np.float64)
+
+
 def codes_and_scale(p: np.ndarray, r, fmt: str):
     """p fp64 [M, K], r fp64 [M] or 1: (codes int8 / uint8 [M, K], scale fp32 [M])."""
     p = np.asarray(p, np.float64)
@@ -34,7 +40,7 @@ def codes_and_scale(p: np.ndarray, r, fmt: str):
         scale = (P * r / R).astype(np.float32)
         fine = np.isfinite(scale)
         live = fine & (P > 0)
-        t = np.where(live[:, None], R * p / P[:, None], 0.0)
+        t = to_47_bits(np.where(live[:, None], R * p / P[:, None], 0.0))
     if fmt == "q8":
         codes = np.rint(t).astype(np.int8)
     else:

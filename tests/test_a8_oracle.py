@@ -67,3 +67,18 @@ def test_norm_and_product_on_small_cases():
     assert np.allclose(oracle.a8.silu_mul([[0.0, 2.0]], [[5.0, 3.0]]), [[0.0, 6.0 / (1 + np.exp(-2.0))]], rtol=1e-15)
     y, size = oracle.a8.gemm_a8(np.array([[1, -2]]), [0.5], np.array([[3, 4]]), [2.0], [10.0], "q8")
     assert y.tolist() == [[5.0]] and size.tolist() == [[11.0]]
+
+
+@pytest.mark.parametrize("fmt", ["q8", "f8"])
+def test_ties_of_rounded_products(fmt):
+    """Rows of one gate: the codes are those of b / max b, whichever way the gate's fp64 value rounds."""
+    if fmt == "q8":
+        b = np.arange(-127.0, 127.5, 0.5)
+    else:
+        v = oracle.decode_f8(np.arange(0x7F, dtype=np.uint8)).astype(np.float64)
+        b = np.concatenate([v, (v[1:] + v[:-1]) / 2])
+    for a in np.random.default_rng(3).standard_normal(200).astype(np.float32) * 4:
+        codes, _ = oracle.a8.codes_and_scale(oracle.a8.silu_mul(np.full((1, b.size), a), b[None]), 1.0, fmt)
+        t = np.copysign(1.0, a) * b                        # max |b| is R, so this is R b / max |b|
+        want = np.rint(t).astype(np.int8) if fmt == "q8" else oracle.a8.nearest_e4m3(t)
+        assert np.array_equal(codes[0], want)

@@ -172,6 +172,28 @@ def test_quotients_next_to_a_border():
         check_codes(rtq.rms_norm(y, w, EPS, fmt=fmt), p, r, fmt)
 
 
+@pytest.mark.parametrize("fmt", ["q8", "f8"])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_true_ties_of_rounded_products(dtype, fmt):
+    """Rows of one gate, and norms with weights of one value: R p / P is b / max b or x / max x exactly."""
+    if fmt == "q8":
+        b = np.arange(-127.0, 127.5, 0.5)
+    else:
+        v = oracle.decode_f8(np.arange(0x7F, dtype=np.uint8)).astype(np.float64)
+        b = np.concatenate([v, (v[1:] + v[:-1]) / 2])
+    code = (lambda t: np.rint(t).astype(np.int8)) if fmt == "q8" else oracle.a8.nearest_e4m3
+    g = torch.Generator().manual_seed(8)
+    a = (torch.randn(200, 1, generator=g) * 4).to(DTYPES[dtype])
+    rows = torch.from_numpy(b)[None].repeat(200, 1).to(DTYPES[dtype]).to(DEV)
+    assert np.array_equal(host(rows[0]), b)
+    out = rtq.silu_mul(a.repeat(1, b.size).to(DEV), rows, fmt=fmt)
+    want = np.stack([code(np.copysign(1.0, s) * b) for s in a[:, 0].tolist()])
+    assert np.array_equal(out.codes.cpu().numpy(), want)
+    for value in (1.1, 0.3, 2 / 3):
+        out = rtq.rms_norm(rows, torch.full((b.size,), value, device=DEV), EPS, fmt=fmt)
+        assert np.array_equal(out.codes.cpu().numpy(), np.stack([code(b)] * 200))
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_sum_in_place_and_what_lies_around_it(dtype):
     """sum_out may be the residual or x; rows of wider buffers and guards stay as they were."""

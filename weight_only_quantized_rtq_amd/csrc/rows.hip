@@ -11,8 +11,9 @@
 // stream's type), or a / (1 + exp(-a)) * b (gated product). The common factor
 // r cancels in the codes.
 //
-// The codes are those of the fp64 formula, as the weight quantizers' are. Two
-// steps make that cheap:
+// The codes are those of the fp64 formula, as the weight quantizers' are, with
+// quotients closer to a tie than fp64 can tell taken as ties. Two steps make
+// that cheap:
 //  - p * (R / P) is taken in fp32 with a factor slightly below and slightly
 //    above R / P, further apart than the relative error Src::kDelta of the
 //    fp32 quotient. Where both round to the same code that is the code;
@@ -170,9 +171,14 @@ __device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
 template <int OUT>
 struct CodeOf {
     static constexpr float kTop = OUT == kOutQ8 ? 127.0f : 448.0f;
-    // The code of the fp64 quotient R * p / P.
+    // The code of the fp64 quotient R * p / P, first rounded to 47 bits. Rows
+    // hold true ties (elements with the gate of the row's largest, b / b_max =
+    // 9 / 16, or weights of one value); the roundings of p, P, R * p and the
+    // quotient, 2^-53 each, would send those either way. 47 bits bring each
+    // back to the tie, and move no other quotient by more than 2^-48 of it.
     static __device__ __forceinline__ uint32_t exact(double p, double P) {
-        const double t = static_cast<double>(kTop) * p / P;
+        const uint64_t bits = __builtin_bit_cast(uint64_t, static_cast<double>(kTop) * p / P);
+        const double t = __builtin_bit_cast(double, (bits + 32u) & ~uint64_t{63});
         if constexpr (OUT == kOutQ8) return static_cast<uint32_t>(static_cast<int>(__builtin_rint(t))) & 0xffu;
         else return e4m3_pair(round_to_odd(t), 0.0f) & 0xffu;
     }
