@@ -91,6 +91,22 @@ def test_gemm(M, N, K, fmt):
         check(y, x, w, b)
 
 
+# K in every remainder of stages over teams, with whole and partial last stages; few tiles and many
+TEAM_SHAPES = [(150, 2000, 1040), (300, 520, 1152), (77, 1999, 1280), (150, 2000, 1300), (300, 520, 1153), (77, 1999, 1535),
+               (300, 520, 1663), (500, 2040, 1040), (500, 2040, 1280), (490, 2030, 1026), (500, 2040, 1285), (490, 2030, 1409),
+               (500, 2040, 1551), (1400, 2000, 1025), (1400, 2000, 1283), (1400, 1990, 2049)]
+
+
+@pytest.mark.parametrize("fmt", ["q8", "f8"])
+@pytest.mark.parametrize("M,N,K", TEAM_SHAPES)
+def test_sums_of_several_teams(M, N, K, fmt):
+    for dtype, bias in ((torch.float32, True), (torch.bfloat16, False)):
+        x, w, b = dev(*make(M, N, K, fmt, M + N + K, bias))
+        y = rtq.gemm_a8(x, w, bias=b, out_dtype=dtype)
+        check(y, x, w, b)
+        assert torch.equal(y, rtq.gemm_a8(x, w, bias=b, out_dtype=dtype))
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 64, 131071), (20, 40, 131056), (130, 70, 131071), (300, 300, 100000)])
 def test_longest_sums(M, N, K):
     """The largest codes over the longest K: int32 holds the sum."""

@@ -303,16 +303,19 @@ __device__ __forceinline__ void dma16(const uint8_t* src, uint8_t* lds_base) {
 
 // BM x BN outputs by WM x WN waves, stages of 128 of K in S LDS buffers: the
 // next S - 1 stages are copied (DMA to LDS, or through registers, S = 2, where
-// rows are not 16-byte aligned) while one is multiplied.
-template <int KIND, int BM, int BN, int WM, int WN, int S, bool ALIGNED>
-__global__ __launch_bounds__(WM * WN * 64) void tile_kernel(const A8Args args) {
+// rows are not 16-byte aligned) while one is multiplied. KS teams of such
+// waves, each with its own buffers, take every KS-th stage, and their sums
+// meet in LDS at the end: where a CU has one workgroup, a stage takes as long
+// as its copies' latency, and the teams' overlap.
+template <int KIND, int BM, int BN, int WM, int WN, int S, int KS, bool ALIGNED>
+__global__ __launch_bounds__(WM * WN * KS * 64) void tile_kernel(const A8Args args) {
     constexpr int NW = WM * WN, ROWS = BM + BN;
     constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
     constexpr int OPS = ROWS / 8 / NW;                         // 1 KB copies of 8 rows, per wave and stage
     static_assert(ROWS % (8 * NW) == 0 && BM % (8 * NW) == 0, "copies divide over the waves");
     static_assert(NW % 2 == 0 && BM % 16 == 0 && TN % 2 == 0, "keys and pairs of blocks");
     static_assert(ALIGNED || S == 2, "copies through registers run one stage ahead");
-    __shared__ __align__(1024) uint8_t lds[S][ROWS * kBK];     // rows 0 .. BM-1: x, then the weights
+    __shared__ __align__(1024) uint8_t lds_all[KS][S][ROWS * kBK];     // rows 0 .. BM-1: x, then the weights
     int tile;
     const A8Task& t = task_of(args, xcd_remap_split(blockIdx.x, args.total), tile);
     const int K = t.K;
@@ -323,7 +326,9 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(const A8Args args) {
     const int high = min(kBand, tiles_m - band * kBand);
     const int64_t m0 = static_cast<int64_t>(band * kBand + in_band % high) * BM;
     const int n0 = in_band / high * BN;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int team = KS == 1 ? 0 : wave_all / NW, wave = KS == 1 ? wave_all : wave_all % NW;
+    uint8_t(&lds)[S][ROWS * kBK] = lds_all[team];
     const int wm = wave % WM * (TM * 16), wn = wave / WM * (TN * 16);
     const int r16 = lane & 15, g = lane >> 4;
     const uint8_t* xb = t.x + m0 * K;
@@ -346,7 +351,7 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(const A8Args args) {
     }
     i32x4 hold[ALIGNED ? 1 : OPS];
     auto issue = [&](int step, int buf) {
-        const int k0 = step * kBK;
+        const int k0 = (step * KS + team) * kBK;
         const uint8_t *x0 = xb + k0, *w0 = wb + k0;
         if (k0 + kBK <= K) {
 #pragma unroll
@@ -384,13 +389,14 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(const A8Args args) {
     };
 
     typename Acc<KIND>::T acc[TN][TM] = {};
-    const int steps = (K + kBK - 1) / kBK;
+    const int stages = (K + kBK - 1) / kBK;                    // mine: this team's
+    const int steps = (stages + KS - 1) / KS, mine = KS == 1 ? steps : (stages - team + KS - 1) / KS;
     // Every buffer is free at the start, so S stages are on their way; from the
     // second step on each step issues the one that its predecessor made room for.
     constexpr int kStart = ALIGNED ? S : 1;
 #pragma unroll
     for (int j = 0; j < kStart; ++j)
-        if (j < steps) issue(j, j);
+        if (j < mine) issue(j, j);
     settle(0);
     auto stage = [&](int step, auto buf_c) {
         constexpr int buf = decltype(buf_c)::value, ahead = (buf + S - 1) % S;
@@ -401,15 +407,16 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(const A8Args args) {
             // This wave's part of the stage. The stages issued after it may stay
             // in flight: S - 2 of them, at the first step S - 1 (with fewer
             // steps left than that, wait for all).
-            if (step == 0 && steps >= S) wait_vm<(S - 1) * OPS>();
-            else if (S == 2 || step + S - 1 > steps) wait_vm<0>();
+            if (step == 0 && mine >= S) wait_vm<(S - 1) * OPS>();
+            else if (S == 2 || step + S - 1 > mine) wait_vm<0>();
             else wait_vm<(S - 2) * OPS>();
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
         } else {
             __syncthreads();
         }
-        const bool more = step + S - 1 < steps && (!ALIGNED || step > 0);
+        if (KS > 1 && step >= mine) return;
+        const bool more = step + S - 1 < mine && (!ALIGNED || step > 0);
         const uint8_t* xs = lds[buf] + wm * kBK;
         const uint8_t* ws = lds[buf] + (BM + wn) * kBK;
         i32x4 b[TM][2], a[TN][2];
@@ -446,6 +453,29 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(const A8Args args) {
         if constexpr (S > 1) { if (step + 1 < steps) stage(step + 1, std::integral_constant<int, 1 % S>()); }
         if constexpr (S > 2) { if (step + 2 < steps) stage(step + 2, std::integral_constant<int, 2 % S>()); }
         if constexpr (S > 3) { if (step + 3 < steps) stage(step + 3, std::integral_constant<int, 3 % S>()); }
+    }
+
+    if constexpr (KS > 1) {                                    // the teams' sums, in their order
+        typedef typename Acc<KIND>::T V;
+        static_assert(sizeof(V) == 16 && BM * BN * 4 <= S * ROWS * kBK, "a team's sums fit its buffers");
+        __syncthreads();
+        if (team > 0) {
+            V* part = reinterpret_cast<V*>(&lds[0][0]) + wave * (TN * TM * 64) + lane;
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+#pragma unroll
+                for (int q = 0; q < TM; ++q) part[(i * TM + q) * 64] = acc[i][q];
+        }
+        __syncthreads();
+        if (team > 0) return;
+#pragma unroll
+        for (int v = 1; v < KS; ++v) {
+            const V* part = reinterpret_cast<const V*>(&lds_all[v][0][0]) + wave * (TN * TM * 64) + lane;
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+#pragma unroll
+                for (int q = 0; q < TM; ++q) acc[i][q] += part[(i * TM + q) * 64];
+        }
     }
 
     // Lane: m = lane % 16 of each block q; C adjacent n of each group of
@@ -516,10 +546,11 @@ hipError_t launch_kind(A8Args& args, hipStream_t stream) {
         skinny_kernel<KIND, MT, W, ALIGNED><<<number(args, 16 * MT, 16), W * 64, 0, stream>>>(args);
         return hipGetLastError();
     };
-    auto tiles = [&](auto bm, auto bn, auto wm, auto wn, auto stages) {
+    auto tiles = [&](auto bm, auto bn, auto wm, auto wn, auto stages, auto teams) {
         constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value;
         constexpr int WM = decltype(wm)::value, WN = decltype(wn)::value, S = ALIGNED ? decltype(stages)::value : 2;
-        tile_kernel<KIND, BM, BN, WM, WN, S, ALIGNED><<<number(args, BM, BN), WM * WN * 64, 0, stream>>>(args);
+        constexpr int KS = decltype(teams)::value;
+        tile_kernel<KIND, BM, BN, WM, WN, S, KS, ALIGNED><<<number(args, BM, BN), WM * WN * KS * 64, 0, stream>>>(args);
         return hipGetLastError();
     };
     constexpr std::integral_constant<int, 1> c1{};
@@ -534,29 +565,43 @@ hipError_t launch_kind(A8Args& args, hipStream_t stream) {
     // count of blocks of each size. us, int8 to bf16, M x N x K, as graph
     // replays (the count in brackets):
     //   16 x 16 straight to registers / 32 x 64 tiles: 80 x 512 x 512 (160) 3.3 / 3.8;
-    //     64 x 2048 x 8192 (512) 13.8 / 14.3; 80 x 2048 x 2048 (640) 7.5 / 5.7
-    //   one / two blocks of m a wave: 64 x 512 x 8192 (128) 9.8 / 13.3; 64 x 2048 x 8192 (512) 17.4 / 13.8
+    //     96 x 512 x 8192 (192) 9.9 / 11.0; 64 x 2048 x 1024 (512) 4.3 / 4.4; 64 x 2048 x 8192 (512) 13.8 / 12.0
+    //   one / two blocks of m a wave: 96 x 512 x 8192 (192) 9.9 / 13.5; 200 x 512 x 8192 (416) 17.2 / 13.7
+    //   one / two teams on K, 32 x 64: 80 x 2048 x 512 (96) 3.7 / 4.0; 80 x 2048 x 8192 (96) 14.7 / 11.8;
+    //     512 x 2048 x 8192 (512) 20.5 / 23.0; 64 x 64: 512 x 2048 x 8192 (256) 18.8 / 16.0; 1024 x 2048 x 8192 (512) 27.2 / 29.3
     //   32 x 64 / 64 x 64: 700 x 512 x 2048 (176) 6.3 / 7.2; 700 x 2048 x 8192 (704) 29.2 / 25.6
     //   64 x 64 / 128 x 128: 1500 x 512 x 8192 (192) 18.6 / 33.4; 1500 x 2048 x 8192 (768) 43.6 / 36.5
     //   128 x 128 of eight waves and four stages, one a CU / of four waves and
     //     two stages, two a CU: 1500 x 2048 x 8192 (192) 36.5 / 46.2; 3000 x 2048 x 8192 (384) 70.5 / 55.3
     //   128 x 128 / 256 x 256: a round of 512 takes 4/7 of a round of 256 of
     //     the large ones: 1500 x 8192 x 8192 (768, 192) 106.6 / 94.0; 3000 x 8192 x 8192 (1536, 384) 188.7 / 195.9
-    // The same where rows are not 16-byte aligned: 16 x 16 / 32 x 64: 200 x 512 x 2049
-    // (416) 8.3 / 10.6; 300 x 512 x 2049 (608) 12.5 / 10.6.
+    // Where rows are not 16-byte aligned: 16 x 16 / 32 x 64: 200 x 512 x 8190
+    // (416) 18.7 / 24.9; 300 x 512 x 2049 (608) 12.5 / 8.9. One / two / four
+    // teams: 32 x 64, 150 x 2048 x 8190 (160) 41.5 / 30.4 / 24.7; 64 x 64,
+    // 500 x 2048 x 2049 (256) 16.2 / 13.8 / 12.5; 128 x 128 of eight waves,
+    // one team or two of four waves: 2048 x 2048 x 8190 (256) 69.4 / 59.5.
     const int64_t n16 = number(args, 16, 16);
-    bool short_k = false;                                      // the tiles load 16 bytes of a row at a time
-    for (int j = 0; j < args.count; ++j) short_k |= args.task[j].K < 16;
-    if (args.M <= 16 || short_k) return skinny(c1, c8);
-    if (n16 <= 512) return n16 < 384 ? skinny(c1, c8) : skinny(c2, c8);
-    if (number(args, 32, 64) <= 512) return tiles(c32, c64, c2, c2, c4);
-    if (number(args, 64, 64) <= 512) return tiles(c64, c64, c2, c2, c4);
+    bool short_k = false, long_k = false;
+    for (int j = 0; j < args.count; ++j) {
+        short_k |= args.task[j].K < 16;                        // the tiles load 16 bytes of a row at a time
+        long_k |= args.task[j].K > 8 * kBK;
+    }
+    if (args.M <= 16 || short_k || n16 <= 256) return skinny(c1, c8);
+    if (n16 <= 512 && !(ALIGNED && long_k)) return skinny(c2, c8);
+    constexpr std::integral_constant<int, ALIGNED ? 2 : 4> teams{};
+    if (long_k && number(args, 32, 64) <= 256) return tiles(c32, c64, c2, c2, c4, teams);
+    if (long_k && number(args, 64, 64) <= 256) return tiles(c64, c64, c2, c2, c4, teams);
+    if (number(args, 32, 64) <= 512) return tiles(c32, c64, c2, c2, c4, c1);
+    if (number(args, 64, 64) <= 512) return tiles(c64, c64, c2, c2, c4, c1);
     const int64_t n128 = number(args, 128, 128), n256 = number(args, 256, 256);
-    if (n128 <= 256) return tiles(c128, c128, c4, c2, c4);
+    if (n128 <= 256) {
+        if (!ALIGNED && long_k) return tiles(c128, c128, c2, c2, c2, c2);
+        return tiles(c128, c128, c4, c2, c4, c1);
+    }
     const int64_t rounds128 = (n128 + 511) / 512 * 4, rounds256 = (n256 + 255) / 256 * 7;
-    if (rounds128 < rounds256 || !large_pays<KIND, ALIGNED>(args)) return tiles(c128, c128, c2, c2, c2);
-    if constexpr (ALIGNED || KIND != kA8F8Wide) return tiles(c256, c256, c4, c2, c2);
-    return tiles(c128, c128, c2, c2, c2);
+    if (rounds128 < rounds256 || !large_pays<KIND, ALIGNED>(args)) return tiles(c128, c128, c2, c2, c2, c1);
+    if constexpr (ALIGNED || KIND != kA8F8Wide) return tiles(c256, c256, c4, c2, c2, c1);
+    return tiles(c128, c128, c2, c2, c2, c1);
 }
 
 bool task_aligned(const A8Task& t) {
