@@ -296,7 +296,8 @@ rtq_status rtq_block_project_ws(const rtq_block* blocks, int32_t n_blocks, int64
  *   code_k = the code nearest to R * p_k / P (ties to even), P = max_k |p_k|,
  *   scale  = fp32(r * P / R),
  * evaluated as in fp64 (the codes are those of the fp64 quotient, as the
- * weight quantizers' are). A row of zeros gets scale 0 and codes 0. A row that
+ * weight quantizers' are; one within 2^-47 of a tie counts as the tie, so that
+ * true ties of rounded p and P go to even). A row of zeros gets scale 0 and codes 0. A row that
  * holds an infinity or a NaN, or whose scale exceeds fp32, gets scale NaN and
  * codes 0, so every product from it is NaN.
  *
