@@ -107,6 +107,20 @@ def test_sums_of_several_teams(M, N, K, fmt):
         assert torch.equal(y, rtq.gemm_a8(x, w, bias=b, out_dtype=dtype))
 
 
+@pytest.mark.parametrize("M", [60, 150, 300, 700])
+def test_teams_of_long_and_short_sums_in_one_call(M):
+    """A launch that splits a long K has projections of one stage, fewer than its teams, beside it."""
+    for fmt in ("q8", "f8"):
+        for Ks in ((65, 2049, 130), (64, 2048, 128, 512)):
+            projs = []
+            for i, K in enumerate(Ks):
+                x, w, b = dev(*make(M, 200 + 8 * i, K, fmt, M + K, i % 2 == 0))
+                projs.append(rtq.Projection(w, x, torch.empty(M, w.N, device=DEV), b))
+            rtq.project_a8(projs)
+            for p in projs:
+                check(p.y, p.x, p.weight, p.bias)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 64, 131071), (20, 40, 131056), (130, 70, 131071), (300, 300, 100000)])
 def test_longest_sums(M, N, K):
     """The largest codes over the longest K: int32 holds the sum."""
