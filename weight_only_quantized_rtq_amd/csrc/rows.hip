@@ -48,49 +48,115 @@ __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(_Float16 v) { return static_cast<float>(v); }
 __device__ __forceinline__ float to_f(__bf16 v) { return static_cast<float>(v); }
 
-// A chunk as it lies in memory. Loads are kept apart from the conversions, so
-// that a thread's loads are all in flight before the first is waited for; a
-// whole chunk goes through memcpy: one 16-byte access per 16 bytes at any
-// alignment of the row. Zeros past n (n <= 0: no element).
+// Forms of a row: K a multiple of eight, so no chunk is partial; any K from
+// eight; K below eight.
+constexpr int kWhole = 0, kTail = 1, kShort = 2;
+
+// A chunk as it lies in memory. Loads are kept apart from what is done with
+// them, so that a thread's loads are all in flight before the first is waited
+// for; a chunk goes through memcpy: one 16-byte access per 16 bytes at any
+// alignment of the row. A test around the load would be a branch with a wait
+// in it, so a thread without a chunk (k beyond the row) reads the row's first
+// and drops it, and a partial chunk is read as the row's last eight elements.
 template <class T>
 struct Raw {
-    T t[kChunk];
-    // The chunk at k of the row p. WHOLE: a thread without a chunk (k beyond
-    // the row, n = 0) reads the row's first and drops it: a test around the
-    // load would be a branch with a wait in it.
-    template <bool WHOLE>
+    static constexpr int kWords = kChunk * sizeof(T) / 4;
+    uint32_t u[kWords];
+    // The chunk at k of the row p, n = K - k or more than eight elements.
+    template <int FORM>
     __device__ __forceinline__ void load(const T* p, int64_t k, int n) {
-        if constexpr (WHOLE) {
-            constexpr int kWords = sizeof(t) / 4;
-            uint32_t u[kWords];
-            __builtin_memcpy(u, p + (n > 0 ? k : 0), sizeof(t));
-#pragma unroll
-            for (int j = 0; j < kWords; ++j) u[j] = n > 0 ? u[j] : 0u;
-            __builtin_memcpy(t, u, sizeof(t));
-        } else if (n >= kChunk) {
-            __builtin_memcpy(t, p + k, sizeof(t));
-        } else {
+        if constexpr (FORM == kShort) {
+            T t[kChunk];
 #pragma unroll
             for (int j = 0; j < kChunk; ++j) t[j] = j < n ? p[k + j] : static_cast<T>(0.0f);
+            __builtin_memcpy(u, t, sizeof(u));
+        } else {
+            const int64_t at = n >= kChunk ? k : FORM == kTail && n > 0 ? k + n - kChunk : 0;
+            __builtin_memcpy(u, p + at, sizeof(u));
+        }
+        if constexpr (FORM == kWhole) {
+#pragma unroll
+            for (int j = 0; j < kWords; ++j) u[j] = n > 0 ? u[j] : 0u;
+        }
+    }
+    // The same for the norm, with a test around the load of a thread without a
+    // chunk: nothing in the branch waits, and the weights' zeros need no select
+    // that would wait for them before the row's loads are issued (2048 x 4096
+    // bf16: 13.0 us, 14.1 with load(); the gated product of 8192 x 8192 prefers
+    // load(): 64 us, 69 with this).
+    template <int FORM>
+    __device__ __forceinline__ void load_if(const T* p, int64_t k, int n) {
+        if constexpr (FORM == kWhole) {
+#pragma unroll
+            for (int j = 0; j < kWords; ++j) u[j] = 0u;
+            if (n > 0) __builtin_memcpy(u, p + k, sizeof(u));
+        } else {
+            load<FORM>(p, k, n);
+        }
+    }
+    // What load() read beside a partial chunk's n elements goes, zeros take its place.
+    template <int FORM>
+    __device__ __forceinline__ void settle(int n) {
+        if constexpr (FORM == kTail) {
+            if (n >= kChunk) return;
+            const int s = n > 0 ? kChunk - n : kChunk;         // elements to drop
+            if constexpr (sizeof(T) == 2) {
+#pragma unroll
+                for (int j = 0; j < kWords; ++j)
+                    u[j] = s & 1 ? __builtin_amdgcn_alignbyte(j + 1 < kWords ? u[j + 1] : 0u, u[j], 2u) : u[j];
+            }
+#pragma unroll
+            for (int by = 1; by <= kWords; by *= 2) {
+                const bool drop = s & (by * 4 / static_cast<int>(sizeof(T)));
+#pragma unroll
+                for (int j = 0; j < kWords; ++j) u[j] = drop ? (j + by < kWords ? u[j + by] : 0u) : u[j];
+            }
         }
     }
     __device__ __forceinline__ void get(float (&v)[kChunk]) const {
+        T t[kChunk];
+        __builtin_memcpy(t, u, sizeof(u));
 #pragma unroll
         for (int j = 0; j < kChunk; ++j) v[j] = to_f(t[j]);
     }
 };
 
-template <bool WHOLE, class T>
+// The first n (1 .. 7) of eight elements of SIZE bytes, in three pieces at
+// most: one branch each for 4, 2 and 1 elements, the rest moved down.
+template <int SIZE>
+__device__ __forceinline__ void store_some(uint8_t* p, int n, const uint32_t (&u)[2 * SIZE]) {
+    uint32_t left[SIZE];
+#pragma unroll
+    for (int j = 0; j < SIZE; ++j) left[j] = u[j];
+    if (n & 4) {
+        __builtin_memcpy(p, left, 4 * SIZE);
+#pragma unroll
+        for (int j = 0; j < SIZE; ++j) left[j] = u[SIZE + j];
+    }
+    p += (n & 4) * SIZE;
+    if (n & 2) {
+        __builtin_memcpy(p, left, 2 * SIZE);
+        if constexpr (SIZE == 1) left[0] >>= 16;
+        else if constexpr (SIZE == 2) left[0] = left[1];
+        else left[0] = left[2];
+    }
+    if (n & 1) __builtin_memcpy(p + (n & 2) * SIZE, left, SIZE);
+}
+
+template <int FORM, class T>
 __device__ __forceinline__ void store_chunk(T* p, int n, const float (&v)[kChunk]) {
-    if (n >= kChunk) {
+    if (FORM == kWhole ? n > 0 : n >= kChunk) {
         T t[kChunk];
 #pragma unroll
         for (int j = 0; j < kChunk; ++j) t[j] = static_cast<T>(v[j]);
         __builtin_memcpy(p, t, sizeof(t));
-    } else if constexpr (!WHOLE) {
+    } else if (FORM != kWhole && n > 0) {
+        T t[kChunk];
+        uint32_t u[2 * sizeof(T)];
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j)
-            if (j < n) p[j] = static_cast<T>(v[j]);
+        for (int j = 0; j < kChunk; ++j) t[j] = static_cast<T>(v[j]);
+        __builtin_memcpy(u, t, sizeof(t));
+        store_some<sizeof(T)>(reinterpret_cast<uint8_t*>(p), n, u);
     }
 }
 
@@ -229,14 +295,13 @@ __device__ __forceinline__ uint32_t bytes_set(u32x2 d) {
     return mask;
 }
 
-template <bool WHOLE>
+template <int FORM>
 __device__ __forceinline__ void store_codes(uint8_t* p, int n, u32x2 w) {
     if (n >= kChunk) {
         __builtin_memcpy(p, &w, 8);
-    } else if constexpr (!WHOLE) {
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j)
-            if (j < n) p[j] = static_cast<uint8_t>(w[j / 4] >> (8 * (j % 4)));
+    } else if (FORM != kWhole && n > 0) {
+        const uint32_t u[2] = {w[0], w[1]};
+        store_some<1>(p, n, u);
     }
 }
 
@@ -318,12 +383,13 @@ struct PlainOp {
     static __device__ __forceinline__ Src src(const RowArgs& a, int64_t row) {
         return Src{static_cast<const T*>(a.x) + row * a.ldx};
     }
-    template <bool WHOLE>
+    template <int FORM>
     __device__ __forceinline__ void load(const RowArgs& a, int64_t row, int64_t k, int n) {
-        x.template load<WHOLE>(static_cast<const T*>(a.x) + row * a.ldx, k, n);
+        x.template load<FORM>(static_cast<const T*>(a.x) + row * a.ldx, k, n);
     }
-    template <bool WHOLE>
-    __device__ __forceinline__ void values(const RowArgs&, int64_t, int64_t, int, float (&p)[kChunk], uint32_t&) {
+    template <int FORM>
+    __device__ __forceinline__ void values(const RowArgs&, int64_t, int64_t, int n, float (&p)[kChunk], uint32_t&) {
+        x.template settle<FORM>(n);
         x.get(p);
     }
 };
@@ -337,22 +403,24 @@ struct NormOp {
         return a.r ? Src{static_cast<const T*>(a.sum) + row * a.lds, a.weight}
                    : Src{static_cast<const T*>(a.x) + row * a.ldx, a.weight};
     }
-    template <bool WHOLE>
+    template <int FORM>
     __device__ __forceinline__ void load(const RowArgs& a, int64_t row, int64_t k, int n) {
-        x.template load<WHOLE>(static_cast<const T*>(a.x) + row * a.ldx, k, n);
-        if (a.r) r.template load<WHOLE>(static_cast<const T*>(a.r) + row * a.ldr, k, n);
+        x.template load_if<FORM>(static_cast<const T*>(a.x) + row * a.ldx, k, n);
+        if (a.r) r.template load_if<FORM>(static_cast<const T*>(a.r) + row * a.ldr, k, n);
     }
     // h = x + residual in fp32, rounded once to the stream's type: what is
     // stored is what is normalised.
-    template <bool WHOLE>
+    template <int FORM>
     __device__ __forceinline__ void values(const RowArgs& a, int64_t row, int64_t k, int n, float (&h)[kChunk], uint32_t&) {
+        x.template settle<FORM>(n);
         x.get(h);
         if (a.r) {
             float b[kChunk];
+            r.template settle<FORM>(n);
             r.get(b);
 #pragma unroll
             for (int j = 0; j < kChunk; ++j) h[j] = to_f(static_cast<T>(h[j] + b[j]));
-            store_chunk<WHOLE>(static_cast<T*>(a.sum) + row * a.lds + k, n, h);
+            store_chunk<FORM>(static_cast<T*>(a.sum) + row * a.lds + k, n, h);
         }
     }
 };
@@ -365,14 +433,16 @@ struct SiluOp {
     static __device__ __forceinline__ Src src(const RowArgs& a, int64_t row) {
         return Src{static_cast<const T*>(a.x) + row * a.ldx, static_cast<const T*>(a.r) + row * a.ldr};
     }
-    template <bool WHOLE>
+    template <int FORM>
     __device__ __forceinline__ void load(const RowArgs& a, int64_t row, int64_t k, int n) {
-        x.template load<WHOLE>(static_cast<const T*>(a.x) + row * a.ldx, k, n);
-        r.template load<WHOLE>(static_cast<const T*>(a.r) + row * a.ldr, k, n);
+        x.template load<FORM>(static_cast<const T*>(a.x) + row * a.ldx, k, n);
+        r.template load<FORM>(static_cast<const T*>(a.r) + row * a.ldr, k, n);
     }
-    template <bool WHOLE>
-    __device__ __forceinline__ void values(const RowArgs&, int64_t, int64_t, int, float (&p)[kChunk], uint32_t& top_ab) {
+    template <int FORM>
+    __device__ __forceinline__ void values(const RowArgs&, int64_t, int64_t, int n, float (&p)[kChunk], uint32_t& top_ab) {
         float b[kChunk];
+        x.template settle<FORM>(n);
+        r.template settle<FORM>(n);
         x.get(p);
         r.get(b);
 #pragma unroll
@@ -384,9 +454,12 @@ struct SiluOp {
     }
     // Dense rows have no maximum to hide behind: gates below -80 and products
     // that overflow before the sigmoid are taken in fp64.
+    template <int FORM>
     __device__ __forceinline__ void dense(const RowArgs& a, int64_t row, int64_t k, int n, float (&p)[kChunk]) {
         float b[kChunk];
         uint32_t mask = 0;
+        x.template settle<FORM>(n);
+        r.template settle<FORM>(n);
         x.get(p);
         r.get(b);
 #pragma unroll
@@ -413,15 +486,16 @@ struct SiluOp {
 // data. NV = 0: rows of any length, read again for each step. Workgroups take
 // rows in turn; the norm's weight stays in registers across them.
 //
-// Bound by memory: long inputs move at 4.9 to 5.7 TB/s, a copy of 1 GiB at 5.1
-// (bf16 quantizer, 16384 x 8192: 70.9 us, 5.7 TB/s; bf16 norm with its sum,
-// 2048 x 4096: 13.0 us, 4.5 TB/s; bf16 gated product, 8192 x 8192: 68.5 us, 4.9
+// Bound by memory: long inputs move at 4.5 to 5.7 TB/s, a copy of 1 GiB at 5.1
+// (bf16 quantizer, 16384 x 8192: 70.0 us, 5.7 TB/s; bf16 norm with its sum,
+// 2048 x 4096: 13.0 us, 4.5 TB/s; bf16 gated product, 8192 x 8192: 63.8 us, 5.3
 // TB/s). One row of 512 takes 2.3 us: one load, two reductions, one store.
 //
-// WHOLE: K is a multiple of eight, so no chunk is partial. Without it every
-// element of a chunk has a test of its own, which costs more than the work
-// (16384 x 8192 bf16: 17 vector instructions an element instead of 8).
-template <class Op, int OUT, class OutT, int TPR, int NV, bool WHOLE>
+// Rows whose K is no multiple of eight cost the moves of one partial chunk and
+// unaligned accesses (bf16, M K = 2^25, K = 4096 / 4095: quantizer 21.1 / 25.5
+// us, gated product 34.9 / 47.2, norm to codes 55.6 / 70.7; with a test for
+// every element of every chunk instead 31.8, 74.4 and 149.0).
+template <class Op, int OUT, class OutT, int TPR, int NV, int FORM>
 __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void row_kernel(RowArgs a) {
     constexpr int RPB = TPR == 64 ? 4 : 1;
     constexpr bool kNorm = Op::kNorm, kDense = OUT == kOutDense;
@@ -436,7 +510,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void row_kernel(RowArgs a) {
     const int per = NV > 0 ? NV : static_cast<int>((a.K + kChunk * TPR - 1) / (kChunk * TPR));
     auto chunk_k = [&](int i) { return static_cast<int64_t>(i * TPR + lane) * kChunk; };
     auto chunk_n = [&](int64_t k) {                                                       // <= 0: none
-        if constexpr (WHOLE) return k < a.K ? kChunk : 0;
+        if constexpr (FORM == kWhole) return k < a.K ? kChunk : 0;
         else return static_cast<int>(a.K - k < kChunk ? a.K - k : kChunk);
     };
 
@@ -445,7 +519,8 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void row_kernel(RowArgs a) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             Raw<float> g;
-            g.load<WHOLE>(a.weight, chunk_k(i), chunk_n(chunk_k(i)));
+            g.load_if<FORM>(a.weight, chunk_k(i), chunk_n(chunk_k(i)));
+            g.settle<FORM>(chunk_n(chunk_k(i)));
             g.get(w[i]);
         }
     }
@@ -460,24 +535,26 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void row_kernel(RowArgs a) {
 
         auto values = [&](Op& op, int i, float (&x)[kChunk]) {
             const int64_t k = chunk_k(i);
-            if constexpr (Op::kSilu && kDense) op.dense(a, row, k, chunk_n(k), x);
-            else op.template values<WHOLE>(a, row, k, chunk_n(k), x, top_ab);
+            if constexpr (Op::kSilu && kDense) op.template dense<FORM>(a, row, k, chunk_n(k), x);
+            else op.template values<FORM>(a, row, k, chunk_n(k), x, top_ab);
         };
         auto take = [&](int i, float (&x)[kChunk]) {
             Op op;
-            op.template load<WHOLE>(a, row, chunk_k(i), chunk_n(chunk_k(i)));
+            op.template load<FORM>(a, row, chunk_k(i), chunk_n(chunk_k(i)));
             values(op, i, x);
         };
         auto weight = [&](int i) {
             Raw<float> g;
-            g.load<WHOLE>(a.weight, chunk_k(i), chunk_n(chunk_k(i)));
+            g.load_if<FORM>(a.weight, chunk_k(i), chunk_n(chunk_k(i)));
+            g.settle<FORM>(chunk_n(chunk_k(i)));
             g.get(w[0]);
         };
         // The same values once more, of a row that values() has been through.
         auto again = [&](int i, float (&x)[kChunk]) {
             if constexpr (kNorm) {
                 Raw<std::remove_const_t<std::remove_pointer_t<decltype(src.h)>>> h;
-                h.template load<WHOLE>(src.h, chunk_k(i), chunk_n(chunk_k(i)));
+                h.template load_if<FORM>(src.h, chunk_k(i), chunk_n(chunk_k(i)));
+                h.template settle<FORM>(chunk_n(chunk_k(i)));
                 h.get(x);
                 weight(i);
             } else {
@@ -497,7 +574,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void row_kernel(RowArgs a) {
         if constexpr (NV > 0) {
             Op op[NV];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) op[i].template load<WHOLE>(a, row, chunk_k(i), chunk_n(chunk_k(i)));
+            for (int i = 0; i < NV; ++i) op[i].template load<FORM>(a, row, chunk_k(i), chunk_n(chunk_k(i)));
 #pragma unroll
             for (int i = 0; i < NV; ++i) values(op[i], i, v[i]);
             if constexpr (kReduced) {
@@ -546,7 +623,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void row_kernel(RowArgs a) {
 #pragma unroll
                     for (int j = 0; j < kChunk; ++j) x[j] = x[j] * rf * wx[j];
                 }
-                store_chunk<WHOLE>(out + k, n, x);
+                store_chunk<FORM>(out + k, n, x);
             };
             if constexpr (NV > 0) {
 #pragma unroll
@@ -634,7 +711,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void row_kernel(RowArgs a) {
                     c = fast_codes<OUT>(p, lo, hi, d);
                     mask = d[0] | d[1] ? bytes_set(d) : 0u;
                 }
-                store_codes<WHOLE>(out + k, n, c);
+                store_codes<FORM>(out + k, n, c);
                 return n >= kChunk ? mask : mask & ((1u << n) - 1u);
             };
             // The same thread stored these elements' chunk, so the bytes land in this order.
@@ -663,11 +740,11 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void row_kernel(RowArgs a) {
 
 constexpr int64_t kMaxGrid = 1 << 20;
 
-template <class Op, int OUT, class OutT, int TPR, int NV, bool WHOLE = true>
+template <class Op, int OUT, class OutT, int TPR, int NV, int FORM>
 hipError_t launch_rows(const RowArgs& a, hipStream_t stream) {
     constexpr int RPB = TPR == 64 ? 4 : 1;
     const int64_t blocks = (a.M + RPB - 1) / RPB;
-    row_kernel<Op, OUT, OutT, TPR, NV, WHOLE><<<static_cast<uint32_t>(blocks < kMaxGrid ? blocks : kMaxGrid),
+    row_kernel<Op, OUT, OutT, TPR, NV, FORM><<<static_cast<uint32_t>(blocks < kMaxGrid ? blocks : kMaxGrid),
                                                 TPR == 64 ? 256 : TPR, 0, stream>>>(a);
     return hipGetLastError();
 }
@@ -680,30 +757,31 @@ hipError_t launch_rows(const RowArgs& a, hipStream_t stream) {
 // 4 15.5. K = 8192: 256 x 4 71.5 (quantizer, M = 16384) and 69.9 (gated
 // product, M = 8192), 512 x 2 71.8 and 83.7. K = 16384, M = 1024: 512 x 4 32.0
 // / 11.1 / 21.3, 1024 x 2 32.9 / 11.4 / 24.7, 256 x 8 40.9 / 11.4 / 23.6.
-template <class Op, int OUT, class OutT>
+template <class Op, int OUT, class OutT, int FORM>
 hipError_t launch_by_length(const RowArgs& a, hipStream_t stream) {
-    if (a.K % kChunk != 0) {
-        if (a.K <= 64 * 8) return launch_rows<Op, OUT, OutT, 64, 1, false>(a, stream);
-        if (a.K <= 256 * 8) return launch_rows<Op, OUT, OutT, 256, 1, false>(a, stream);
-        if (a.K <= 256 * 32) return launch_rows<Op, OUT, OutT, 256, 4, false>(a, stream);
-        return launch_rows<Op, OUT, OutT, 1024, 0, false>(a, stream);
-    }
-    if (a.K <= 64 * 8) return launch_rows<Op, OUT, OutT, 64, 1>(a, stream);
-    if (a.K <= 64 * 16) return launch_rows<Op, OUT, OutT, 64, 2>(a, stream);
-    if (a.K <= 128 * 16) return launch_rows<Op, OUT, OutT, 128, 2>(a, stream);
-    if (a.K <= 256 * 16) return launch_rows<Op, OUT, OutT, 256, 2>(a, stream);
-    if (a.K <= 256 * 32) return launch_rows<Op, OUT, OutT, 256, 4>(a, stream);
-    if (a.K <= 512 * 32) return launch_rows<Op, OUT, OutT, 512, 4>(a, stream);
-    return launch_rows<Op, OUT, OutT, 1024, 0>(a, stream);
+    if (a.K <= 64 * 8) return launch_rows<Op, OUT, OutT, 64, 1, FORM>(a, stream);
+    if (a.K <= 64 * 16) return launch_rows<Op, OUT, OutT, 64, 2, FORM>(a, stream);
+    if (a.K <= 128 * 16) return launch_rows<Op, OUT, OutT, 128, 2, FORM>(a, stream);
+    if (a.K <= 256 * 16) return launch_rows<Op, OUT, OutT, 256, 2, FORM>(a, stream);
+    if (a.K <= 256 * 32) return launch_rows<Op, OUT, OutT, 256, 4, FORM>(a, stream);
+    if (a.K <= 512 * 32) return launch_rows<Op, OUT, OutT, 512, 4, FORM>(a, stream);
+    return launch_rows<Op, OUT, OutT, 1024, 0, FORM>(a, stream);
+}
+
+template <class Op, int OUT, class OutT>
+hipError_t launch_by_form(const RowArgs& a, hipStream_t stream) {
+    if (a.K % kChunk == 0) return launch_by_length<Op, OUT, OutT, kWhole>(a, stream);
+    if (a.K > kChunk) return launch_by_length<Op, OUT, OutT, kTail>(a, stream);
+    return launch_rows<Op, OUT, OutT, 64, 1, kShort>(a, stream);
 }
 
 template <template <class> class Op, class T>
 hipError_t launch_by_out(const RowArgs& a, int fmt, int out_dtype, hipStream_t stream) {
-    if (fmt == RTQ_FMT_Q8) return launch_by_length<Op<T>, kOutQ8, uint8_t>(a, stream);
-    if (fmt == RTQ_FMT_F8) return launch_by_length<Op<T>, kOutF8, uint8_t>(a, stream);
+    if (fmt == RTQ_FMT_Q8) return launch_by_form<Op<T>, kOutQ8, uint8_t>(a, stream);
+    if (fmt == RTQ_FMT_F8) return launch_by_form<Op<T>, kOutF8, uint8_t>(a, stream);
     if constexpr (!__is_same(Op<T>, PlainOp<T>)) {
-        if (out_dtype == RTQ_F32) return launch_by_length<Op<T>, kOutDense, float>(a, stream);
-        return launch_by_length<Op<T>, kOutDense, T>(a, stream);
+        if (out_dtype == RTQ_F32) return launch_by_form<Op<T>, kOutDense, float>(a, stream);
+        return launch_by_form<Op<T>, kOutDense, T>(a, stream);
     }
     return hipErrorInvalidValue;
 }
