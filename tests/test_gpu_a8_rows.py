@@ -220,6 +220,33 @@ def test_sum_in_place_and_what_lies_around_it(dtype):
     assert (codes[0] == 77).all() and (codes[-1] == 77).all() and scale[0] == 5 and scale[-1] == 5
 
 
+@pytest.mark.parametrize("K", [3, *range(9, 17), *range(513, 520), 1021, 4094, 9003, 16391])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_partial_chunks_in_place_and_their_neighbours(dtype, K):
+    """Every remainder of K by eight: codes, the sum in place and dense rows, with guards on both sides."""
+    M = 5
+    w = 1 + 0.1 * torch.randn(K, generator=torch.Generator().manual_seed(K)).to(DEV)
+    wide, other = make(M + 2, K + 3, dtype, K).contiguous(), make(M, K, dtype, K + 1)
+    inner, before = wide[1:M + 1, 2:K + 2], wide.clone()
+    h, p, r = oracle.a8.rms_norm_parts(host(inner), host(other), host(w), EPS, dtype)
+    codes = torch.full((M + 2, K), 77, dtype=torch.uint8, device=DEV)
+    scale = torch.full((M + 2,), 5.0, device=DEV)
+    out = rtq.A8Rows(codes[1:M + 1], scale[1:M + 1])
+    rtq.rms_norm(inner, w, EPS, residual=other, fmt="f8", sum_out=inner, out=out)
+    check_codes(out, p, r, "f8")
+    assert np.array_equal(host(inner), h)
+    before[1:M + 1, 2:K + 2] = inner
+    assert torch.equal(before, wide)
+    assert (codes[0] == 77).all() and (codes[-1] == 77).all() and scale[0] == 5 and scale[-1] == 5
+    dense = torch.full((M + 2, K), 3.0, dtype=DTYPES[dtype], device=DEV)
+    rtq.rms_norm(inner, w, EPS, out=dense[1:M + 1])
+    h, p, r = oracle.a8.rms_norm_parts(host(inner), None, host(w), EPS, dtype)
+    check_dense(dense[1:M + 1], p * r[:, None], 3)
+    rtq.silu_mul(inner, other, out=dense[1:M + 1])
+    check_dense(dense[1:M + 1], oracle.a8.silu_mul(host(inner), host(other)), 8)
+    assert (dense[0] == 3).all() and (dense[-1] == 3).all()
+
+
 def test_empty_and_many_rows():
     w = torch.ones(8, device=DEV)
     x = torch.empty(0, 8, device=DEV)
